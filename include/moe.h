@@ -141,6 +141,26 @@ MOE_API size_t moe_weights_prepared_size_w(moe_wtype w_type, int n_experts, int 
 MOE_API moe_status moe_weights_prepare_w(moe_wtype w_type, const void *blocks, int n_experts, int n_out, int n_in,
                                          void *prepared, moe_stream stream);
 
+/*
+ * Quantise rows to the MXFP4 blocks described at moe_wtype (the form that
+ * moe_weights_prepare_w reads).  x: [n_rows][n] of x_type, rows row_stride
+ * elements apart (row_stride >= n, n % 32 == 0); blocks: 17 bytes per 32
+ * values, [n_rows][n/32][17], any alignment.  Per block, amax its largest
+ * magnitude:
+ *   X = max(floor(log2 amax) - 2, -127) + 127   (X = 0 where amax == 0)
+ *   code of v = v / 2^(X-127) rounded to the nearest E2M1 value, ties to the
+ *               even code, magnitudes above 6 to 6; the sign bit is v's own
+ * (a pure function of the values, no tolerance).  A block that holds a NaN or
+ * an infinity gets X = 255 and codes 0.  values, if not NULL: what the blocks
+ * stand for, [n_rows][n] of x_type without gaps, 16-byte aligned (exact; NaN
+ * for X = 255).  blocks and values must not overlap x.  Errors (host):
+ * MOE_ERR_INVALID for null pointers, an unknown type, n or row_stride out of
+ * range, x not aligned to its type or values to 16 bytes; MOE_ERR_RANGE for
+ * n_rows >= 2^31, row_stride >= 2^40 or 2^37 blocks.  n_rows == 0 does nothing.
+ */
+MOE_API moe_status moe_mxfp4_quantize(const void *x, moe_dtype x_type, int64_t row_stride, int64_t n_rows, int n,
+                                      void *blocks, void *values, moe_stream stream);
+
 /* ------------------------------------------------------------------ row ids */
 
 /*
@@ -246,6 +266,20 @@ MOE_API moe_status moe_ffn_decode_noalloc(const void *Wg, const void *Wu, const 
                                           const void *x, moe_dtype x_type, const int32_t *ids, int64_t n_tokens, int k,
                                           float *dst, float *dst_shared, int *status_out, moe_stream stream);
 
+/*
+ * The indirect product with both operands in MXFP4: x is rounded to MXFP4
+ * blocks along n_in exactly as moe_mxfp4_quantize rounds, and
+ *   dst[t][s][:] = W[ids[t][s]] . Q(x[r]),   r = t (broadcast) or (t, s) (per_slot).
+ * Products of the rounded operands are exact; sums are float.  A block of x
+ * that holds a NaN or an infinity makes its token's results NaN.  W_prepared
+ * comes from moe_weights_prepare_w(MOE_MXFP4, ...); layouts, limits, errors and
+ * the workspace (moe_workspace_size with n_hidden = 0) are those of
+ * moe_mul_mat_id.
+ */
+MOE_API moe_status moe_mul_mat_id_mx4(const void *W_prepared, int n_experts, int n_out, int n_in, const void *x,
+                                      moe_dtype x_type, const int32_t *ids, int64_t n_tokens, int k, moe_mode mode,
+                                      float *dst, void *workspace, moe_stream stream);
+
 /* ------------------------------------------------------------------ router */
 
 /*
@@ -274,6 +308,63 @@ MOE_API moe_status moe_ffn_decode_noalloc(const void *Wg, const void *Wu, const 
 MOE_API moe_status moe_route(const float *logits, const float *bias, int64_t n_tokens, int n_experts, int k,
                              int normalize, int32_t *ids, float *weights, moe_stream stream);
 
+/*
+ * Scored router: moe_route for layers whose router scores the experts by a
+ * sigmoid or a softmax, uses a balance bias on the scores for the choice only,
+ * and may choose within the best groups of experts.  With scores s of token t
+ * (MOE_SIGMOID: s[e] = 1 / (1 + exp(-l[e])); MOE_SOFTMAX: over all experts):
+ *   key[e]  = s[e] + bias[e]                 (bias may be NULL: s[e])
+ *   group g = experts [g*m, (g+1)*m), m = n_experts / n_groups; its score is its
+ *             largest key (group_top = 1) or the sum of its two largest
+ *             (group_top = 2); the topk_groups groups of largest score are open
+ *             (equal scores: the lower group first)
+ *   ids[t][:]     = the k largest keys of open groups, descending, equal keys in
+ *                   ascending expert index                (int32 [n_tokens][k])
+ *   weights[t][i] = scale * s[ids[i]], divided by the sum of the k chosen s when
+ *                   normalize != 0                        (float [n_tokens][k])
+ * n_groups = topk_groups = 1 chooses among all experts.  The choice follows the
+ * rule over real numbers (keys that close float values cannot tell apart are
+ * compared in double); without a bias equal logits are equal keys.  Weights are
+ * evaluated in float relative to the largest logit involved, so normalised
+ * weights stay finite and sum to scale however far the logits are from zero:
+ * within (span + 16 + n_experts + k) * 2^-24 relative of the exact value, span
+ * the largest minus the smallest finite logit involved.  A logit of -inf has
+ * score 0 (and key bias[e]); where all scores of a sum are 0 the weights are 0.
+ * NaN or +inf logits: ids are still k distinct experts of open groups, weights
+ * unspecified.  logits: l_type, rows row_stride elements apart; bias float.
+ * Errors (host): MOE_ERR_INVALID for null pointers, unknown enums, k outside
+ * [1, topk_groups*m], row_stride < n_experts, n_groups that does not divide
+ * n_experts, topk_groups outside [1, n_groups], group_top outside [1, min(2, m)],
+ * misalignment; MOE_ERR_RANGE for n_tokens >= 2^22, n_experts > 1024,
+ * k >= 1024, n_groups > 32 or row_stride >= 2^40.  n_tokens == 0 does nothing.
+ */
+typedef enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
+MOE_API moe_status moe_route_scored(const void *logits, moe_dtype l_type, int64_t row_stride, const float *bias,
+                                    int64_t n_tokens, int n_experts, int k, moe_score score, int n_groups,
+                                    int topk_groups, int group_top, int normalize, float scale, int32_t *ids,
+                                    float *weights, moe_stream stream);
+
+/*
+ * Gradient of moe_route_scored's weights with respect to the logits, for the
+ * same score, normalize and scale and the ids that it gave (the choice, and so
+ * the bias and the groups, have no gradient).  With g = scale * dweights[t] and
+ * p_i = s_i / (sum of the chosen s):
+ *   sigmoid, normalised:  dl[ids_i] = p_i (g_i - sum_j g_j p_j) (1 - s_i)
+ *   sigmoid:              dl[ids_i] = g_i s_i (1 - s_i)
+ *   softmax, normalised:  dl[ids_i] = p_i (g_i - sum_j g_j p_j)
+ *   softmax:              dl[e] = s_e ([e = ids_i] g_i - sum_j g_j s_{ids_j}),
+ * the other entries 0.  dweights: float [n_tokens][k]; dlogits: l_type
+ * [n_tokens][n_experts] without gaps, every element written; it must not
+ * overlap the inputs.  Evaluated in float, rounded to l_type once.  A slot
+ * whose id is outside [0, n_experts) is left out (-1 marks an unused slot);
+ * an id that occurs twice in a token adds up.  Entries of -inf logits are 0.
+ * Errors as for moe_route_scored.
+ */
+MOE_API moe_status moe_route_scored_backward(const void *logits, moe_dtype l_type, int64_t row_stride,
+                                             const int32_t *ids, const float *dweights, int64_t n_tokens,
+                                             int n_experts, int k, moe_score score, int normalize, float scale,
+                                             void *dlogits, moe_stream stream);
+
 /* ----------------------------------------------------------------- combine */
 
 /*
@@ -297,6 +388,21 @@ MOE_API moe_status moe_route(const float *logits, const float *bias, int64_t n_t
  */
 MOE_API moe_status moe_combine(const float *dst, const float *weights, const float *dst_shared, int64_t n_tokens,
                                int k, int64_t n, float *y, moe_stream stream);
+
+/*
+ * Gradient of moe_combine.  With dy float [n_tokens][n] the gradient of y:
+ *   dweights[t][s] = sum_j dy[t][j] * dst[t][s][j]       (float [n_tokens][k])
+ *   ddst[t][s][j]  = weights[t][s] * dy[t][j]            (float [n_tokens][k][n])
+ * (that of dst_shared is dy itself).  ddst may be NULL: dweights alone, as for
+ * training a router over frozen experts.  dy, dst, weights: the layouts of
+ * moe_combine, 4-byte aligned; 16-byte alignment and n % 4 == 0 take the vector
+ * path.  The outputs must not overlap the inputs, except that ddst may be dst
+ * itself.  Sums are float in a fixed order: bit-identical from run to run,
+ * within (n / 256 + 16) * 2^-24 * sum of the terms' magnitudes of the exact sum.
+ * Errors as for moe_combine.
+ */
+MOE_API moe_status moe_combine_backward(const float *dy, const float *dst, const float *weights, int64_t n_tokens,
+                                        int k, int64_t n, float *dweights, float *ddst, moe_stream stream);
 
 /* ------------------------------------------------------------------ tuning */
 

@@ -20,6 +20,9 @@ OK, ERR_INVALID, ERR_RANGE, ERR_BAD_ID, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED =
 BROADCAST, PER_SLOT = 0, 1
 BF16, F16, F32 = 0, 1, 2
 Q8_0, MXFP4 = 0, 1
+SOFTMAX, SIGMOID = 0, 1
+_SCORE = {"softmax": SOFTMAX, "sigmoid": SIGMOID, SOFTMAX: SOFTMAX, SIGMOID: SIGMOID}
+_GROUP_TOP = {"max": 1, "top2": 2, 1: 1, 2: 2}
 _WTYPE = {"q8_0": Q8_0, "mxfp4": MXFP4, Q8_0: Q8_0, MXFP4: MXFP4}
 
 # every symbol declared in include/moe.h
@@ -28,11 +31,13 @@ ABI_SYMBOLS = (
     "moe_weights_prepared_size", "moe_weights_prepare", "moe_row_ids", "moe_mul_mat_id", "moe_ffn",
     "moe_ffn_decode_noalloc", "moe_route", "moe_combine", "moe_set_gemv_threshold", "moe_get_gemv_threshold",
     "moe_set_path", "moe_profile_enable", "moe_profile_read", "moe_weights_prepared_size_w", "moe_weights_prepare_w",
-    "moe_mul_mat_id_w", "moe_ffn_w", "moe_testing_stall",
+    "moe_mul_mat_id_w", "moe_ffn_w", "moe_testing_stall", "moe_mxfp4_quantize", "moe_mul_mat_id_mx4",
+    "moe_route_scored", "moe_route_scored_backward", "moe_combine_backward",
 )
 
 _lib = None
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 def _L() -> ctypes.CDLL:
@@ -66,6 +71,12 @@ def _L() -> ctypes.CDLL:
                                          _i32, _vp, _vp, _vp, _vp]
     L.moe_route.argtypes = [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]
     L.moe_combine.argtypes = [_vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp]
+    L.moe_mxfp4_quantize.argtypes = [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp]
+    L.moe_mul_mat_id_mx4.argtypes = [_vp, _i32, _i32, _i32, _vp, _i32, _vp, _i64, _i32, _i32, _vp, _vp, _vp]
+    L.moe_route_scored.argtypes = [_vp, _i32, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp,
+                                   _vp, _vp]
+    L.moe_route_scored_backward.argtypes = [_vp, _i32, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _f32, _vp, _vp]
+    L.moe_combine_backward.argtypes = [_vp, _vp, _vp, _i64, _i32, _i64, _vp, _vp, _vp]
     L.moe_set_gemv_threshold.argtypes = [_i32]
     L.moe_set_gemv_threshold.restype = None
     L.moe_get_gemv_threshold.argtypes = []
@@ -141,6 +152,33 @@ def _need(t, name, dtype, numel, device=None):
     return t
 
 
+def _call(what, dev, fn, *args):
+    """Run an entry point with `dev` current and its current stream as the last
+    argument (a launch needs its stream's device to be the current one)."""
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != OK:
+        raise MoeError(rc, what)
+
+
+def _rows(t, name):
+    """(n_rows, n, row stride) of a CUDA tensor whose last dimension has no
+    gaps: contiguous, or two-dimensional with rows a fixed stride apart."""
+    _gpu(t, name)
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    n = t.shape[-1]
+    rows = t.numel() // n if n else 0
+    if t.is_contiguous():
+        return rows, n, max(n, 1)
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < n:
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return rows, n, t.stride(0) if rows > 1 else n
+
+
 # ----------------------------------------------------------------- memory
 def workspace_size(n_tokens, k, n_experts, n_in, n_hidden=0, n_hidden_shared=0, x_dtype=torch.bfloat16) -> int:
     return _L().moe_workspace_size(n_tokens, k, n_experts, n_in, n_hidden, n_hidden_shared, _XTYPE[x_dtype])
@@ -179,6 +217,33 @@ def weights_prepare(blocks, n_experts, n_out, n_in, out=None, wtype="q8_0"):
     _chk(_L().moe_weights_prepare_w(w, _ptr(blocks), n_experts, n_out, n_in, _ptr(out), _stream(blocks.device)),
          "moe_weights_prepare")
     return out
+
+
+def mxfp4_quantize(x, with_values=False, out=None, values=None):
+    """Quantise to MXFP4 blocks along the last dimension (moe_mxfp4_quantize).
+
+    x: CUDA tensor [..., n] of bfloat16, float16 or float32, n % 32 == 0,
+    contiguous or two-dimensional with strided rows.  Returns blocks uint8
+    [..., n/32][17] (what weights_prepare takes with wtype "mxfp4").  With
+    `with_values`, or with `values` given, also returns the values the blocks
+    stand for, [..., n] of x's type: (blocks, values)."""
+    rows, n, ld = _rows(x, "x")
+    if x.dtype not in _XTYPE:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    if n % 32 or n == 0:
+        raise ValueError("the last dimension of x must be a positive multiple of 32")
+    dev = x.device
+    shape = tuple(x.shape)
+    if out is None:
+        out = torch.empty(shape[:-1] + (n // 32, 17), dtype=torch.uint8, device=dev)
+    _need(out, "out", torch.uint8, rows * (n // 32) * 17, dev)
+    if values is None and with_values:
+        values = torch.empty(shape, dtype=x.dtype, device=dev)
+    if values is not None:
+        _need(values, "values", x.dtype, rows * n, dev)
+    _call("moe_mxfp4_quantize", dev, _L().moe_mxfp4_quantize, x.data_ptr(), _XTYPE[x.dtype], ld, rows, n,
+          out.data_ptr(), None if values is None else values.data_ptr())
+    return out if values is None else (out, values)
 
 
 # ----------------------------------------------------------------- row ids
@@ -224,6 +289,34 @@ def mul_mat_id(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None, out
                                _MODE[mode], _ptr(out), _ptr(ws), _stream(x.device)), "moe_mul_mat_id")
     if own_ws:
         _chk(get_status(ws), "moe_mul_mat_id (device status)")
+    return out
+
+
+def mul_mat_id_mx4(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None, out=None):
+    """dst float32 [T][k][n_out] = W[ids[t][s]] . Q(x[t or (t, s)]), both operands
+    in MXFP4 (moe_mul_mat_id_mx4): W prepared with wtype "mxfp4", x rounded to
+    MXFP4 blocks by the call as mxfp4_quantize rounds.
+
+    Arguments, workspace and errors as for mul_mat_id."""
+    _cuda(x, "x")
+    if x.dtype not in _XTYPE:
+        raise ValueError("x must be bfloat16, float16 or float32")
+    dev = x.device
+    _cuda(ids, "ids", torch.int32, dev)
+    T, k = ids.shape
+    _need(W, "W", torch.uint8, weights_prepared_size(n_experts, n_out, n_in, MXFP4), dev)
+    _need(x, "x", x.dtype, (T if _MODE[mode] == BROADCAST else T * k) * n_in)
+    own_ws = ws is None
+    if own_ws:
+        ws = workspace(T, k, n_experts, n_in, x_dtype=x.dtype, device=dev)
+    _need(ws, "ws", torch.uint8, workspace_size(T, k, n_experts, n_in, x_dtype=x.dtype), dev)
+    if out is None:
+        out = torch.empty((T, k, n_out), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.float32, T * k * n_out, dev)
+    _call("moe_mul_mat_id_mx4", dev, _L().moe_mul_mat_id_mx4, W.data_ptr(), n_experts, n_out, n_in, x.data_ptr(),
+          _XTYPE[x.dtype], ids.data_ptr(), T, k, _MODE[mode], out.data_ptr(), ws.data_ptr())
+    if own_ws:
+        _chk(get_status(ws), "moe_mul_mat_id_mx4 (device status)")
     return out
 
 
@@ -320,6 +413,86 @@ def route(logits, k, bias=None, normalize=True, ids=None, weights=None):
     _chk(_L().moe_route(_ptr(logits), _ptr(bias), T, E, k, 1 if normalize else 0, _ptr(ids), _ptr(weights),
                         _stream(logits.device)), "moe_route")
     return ids, weights
+
+
+def route_scored(logits, k, bias=None, score="sigmoid", n_groups=1, topk_groups=1, group_score="max",
+                 normalize=True, scale=1.0, ids=None, weights=None):
+    """Scored router through moe_route_scored: the k largest score + bias per
+    token, within the topk_groups best of n_groups groups of experts, and the
+    scores as weights (divided by their sum with `normalize`, times `scale`).
+
+    logits: CUDA [T][E] of float32, bfloat16 or float16, rows may be strided;
+    score: "sigmoid" or "softmax"; bias: float32 [E] or None (choice only);
+    group_score: "max" or "top2" (sum of a group's two largest keys).
+    Returns (ids int32 [T][k], weights float32 [T][k])."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in _XTYPE:
+        raise ValueError("logits must be a [T][E] tensor of float32, bfloat16 or float16")
+    T, E, ld = _rows(logits, "logits")
+    dev = logits.device
+    if bias is not None:
+        _need(bias, "bias", torch.float32, E, dev)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _need(ids, "ids", torch.int32, T * k, dev)
+    _need(weights, "weights", torch.float32, T * k, dev)
+    _call("moe_route_scored", dev, _L().moe_route_scored, logits.data_ptr(), _XTYPE[logits.dtype], ld,
+          None if bias is None else bias.data_ptr(), T, E, k, _SCORE[score], n_groups, topk_groups,
+          _GROUP_TOP[group_score], 1 if normalize else 0, scale, ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def route_scored_backward(logits, ids, dweights, score="sigmoid", normalize=True, scale=1.0, out=None):
+    """Gradient of route_scored's weights with respect to the logits, through
+    moe_route_scored_backward: logits as in the forward call, ids the int32
+    [T][k] that it gave (a slot with an id outside [0, E) is left out),
+    dweights float32 [T][k].  Returns dlogits [T][E] of the logits' type."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.dtype not in _XTYPE:
+        raise ValueError("logits must be a [T][E] tensor of float32, bfloat16 or float16")
+    T, E, ld = _rows(logits, "logits")
+    dev = logits.device
+    _cuda(ids, "ids", torch.int32, dev)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError("ids must be [T][k]")
+    k = ids.shape[1]
+    _need(dweights, "dweights", torch.float32, T * k, dev)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _need(out, "out", logits.dtype, T * E, dev)
+    _call("moe_route_scored_backward", dev, _L().moe_route_scored_backward, logits.data_ptr(), _XTYPE[logits.dtype],
+          ld, ids.data_ptr(), dweights.data_ptr(), T, E, k, _SCORE[score], 1 if normalize else 0, scale,
+          out.data_ptr())
+    return out
+
+
+def combine_backward(dy, dst, weights, need_ddst=True, dweights=None, ddst=None):
+    """Gradient of combine through moe_combine_backward.  dy: float32 CUDA [T][n];
+    dst: float32 [T][k][n] (or [T*k][n]); weights: float32 [T][k].  Returns
+    (dweights [T][k], ddst of dst's shape, or None without `need_ddst`); the
+    gradient of the shared term is dy itself.  ddst may be dst."""
+    _cuda(dst, "dst", torch.float32)
+    dev = dst.device
+    _cuda(weights, "weights", torch.float32, dev)
+    if weights.dim() != 2:
+        raise ValueError("weights must be [T][k]")
+    T, k = weights.shape
+    n = dst.shape[-1]
+    if dst.numel() != T * k * n:
+        raise ValueError("dst must hold n_tokens*k rows of n")
+    _need(dy, "dy", torch.float32, T * n, dev)
+    if dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _need(dweights, "dweights", torch.float32, T * k, dev)
+    if not need_ddst:
+        ddst = None
+    elif ddst is None:
+        ddst = torch.empty_like(dst)
+    if ddst is not None:
+        _need(ddst, "ddst", torch.float32, T * k * n, dev)
+    _call("moe_combine_backward", dev, _L().moe_combine_backward, dy.data_ptr(), dst.data_ptr(), weights.data_ptr(),
+          T, k, n, dweights.data_ptr(), None if ddst is None else ddst.data_ptr())
+    return dweights, ddst
 
 
 def combine(dst, weights, shared=None, out=None):

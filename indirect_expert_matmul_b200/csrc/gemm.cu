@@ -926,13 +926,14 @@ static moe_status gather(const void* x, int x_type, int n_in, const int32_t* src
 
 moe_status launch_gemm_mul_mat_id(const GemmMulMatId& g, cudaStream_t stream) {
     const int mx = g.wtype == MOE_MXFP4;  // bf16 operands, unscaled activation rows
-    moe_status st = g.x_rows * g.k == g.S
+    moe_status st = g.xt_ready ? MOE_OK
+                    : g.x_rows * g.k == g.S
                         ? gather_tokens(g.x, g.x_type, g.n_in, g.slot_prow, g.k, g.x_rows, g.rows_pad, g.xt, g.xs,
                                         g.hdr, mx, stream)
                         : gather(g.x, g.x_type, g.n_in, g.ids_src1, g.bounds, g.pad_start, g.E, g.S, g.rows_pad, g.xt,
                                  g.xs, g.hdr, mx, stream);
     if (st) return st;
-    prof_mark(stream, "gather");
+    if (!g.xt_ready) prof_mark(stream, "gather");
     GemmParams p = {};
     p.A0 = g.W;
     p.L = WLayout(g.n_out, g.n_in, g.wtype);

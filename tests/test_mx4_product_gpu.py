@@ -1,0 +1,200 @@
+"""moe_mul_mat_id_mx4 against a 64-bit implementation.  The operands are exact
+(x is rounded to MXFP4 by a rule without tolerance), so only the float32 sum
+remains: n_in additions, each off by at most one unit in the last place of a
+partial sum, which is at most the sum of the terms' magnitudes - a bound of
+n_in * 2^-23 * sum |w x|."""
+import numpy as np
+import pytest
+import torch
+
+import indirect_expert_matmul_b200 as moe
+from tests import routed_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def _weights(E, n_out, n_in, seed, lo=117, hi=123):
+    g = torch.Generator().manual_seed(seed)
+    b = torch.randint(0, 256, (E, n_out, n_in // 32, 17), generator=g, dtype=torch.uint8)
+    b[..., 0] = torch.randint(lo, hi, (E, n_out, n_in // 32), generator=g, dtype=torch.uint8)
+    return b
+
+
+def _ids(T, k, E, seed, only=None):
+    g = torch.Generator().manual_seed(seed)
+    pool = torch.arange(E) if only is None else torch.tensor(only)
+    return torch.stack([pool[torch.randperm(len(pool), generator=g)[:k]] for _ in range(T)]).int()
+
+
+def _run(blocks, x, ids, mode, **kw):
+    E, n_out, nb, _ = blocks.shape
+    W = moe.weights_prepare(blocks.cuda(), E, n_out, nb * 32, wtype="mxfp4")
+    return moe.mul_mat_id_mx4(W, E, n_out, nb * 32, x, ids.cuda(), mode=mode, **kw)
+
+
+def _check(blocks, x, ids, mode):
+    dst = _run(blocks, x, ids, mode)
+    out, mag = ref.mx_product(blocks.numpy(), x.double().cpu().numpy(), ids.numpy(), mode == "per_slot")
+    err = np.abs(dst.double().cpu().numpy() - out)
+    n_in = blocks.shape[2] * 32
+    tol = n_in * 2.0 ** -23 * mag
+    assert (err <= tol).all(), (float((err / np.maximum(tol, 1e-300)).max()), np.argwhere(~(err <= tol))[:4].tolist())
+    dst2 = _run(blocks, x, ids, mode)
+    assert torch.equal(dst.view(torch.int32), dst2.view(torch.int32))
+    return dst
+
+
+@pytest.mark.parametrize("mode", ["broadcast", "per_slot"])
+@pytest.mark.parametrize("T,E,k,n_in,n_out,dtype", [
+    (1, 1, 1, 32, 1, "f32"), (1, 8, 2, 32, 16, "bf16"), (1, 16, 8, 2048, 512, "bf16"), (4, 32, 8, 256, 130, "f16"),
+    (3, 4, 2, 96, 33, "f32"), (8, 8, 4, 352, 144, "bf16"), (40, 4, 2, 512, 260, "bf16"), (65, 3, 3, 160, 129, "f32"),
+    (300, 2, 1, 288, 128, "f16"), (257, 5, 4, 1408, 96, "bf16"), (130, 60, 6, 128, 200, "f32"),
+    (17, 300, 10, 64, 40, "bf16")])
+def test_product(mode, T, E, k, n_in, n_out, dtype):
+    blocks = _weights(E, n_out, n_in, n_in + n_out)
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T if mode == "broadcast" else T * k, n_in, generator=g).to(DT[dtype]).cuda()
+    _check(blocks, x, _ids(T, k, E, T + E), mode)
+
+
+def test_one_expert_takes_all_and_most_take_none():
+    blocks = _weights(64, 64, 192, 1)
+    x = torch.randn(600, 192, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    ids = torch.full((600, 1), 37, dtype=torch.int32)
+    _check(blocks, x, ids, "broadcast")
+    ids[::50] = 63
+    _check(blocks, x, ids, "broadcast")
+
+
+def test_the_same_expert_twice_in_a_token():
+    blocks = _weights(4, 40, 64, 5)
+    x = torch.randn(3, 64, generator=torch.Generator().manual_seed(6)).cuda()
+    _check(blocks, x, torch.tensor([[1, 1], [0, 3], [2, 2]], dtype=torch.int32), "broadcast")
+
+
+@pytest.mark.parametrize("T", [2, 70])
+def test_wide_scales_and_zero_blocks(T):
+    # block scales far apart in both operands, whole blocks of zeros, and a row of zeros
+    g = torch.Generator().manual_seed(8)
+    blocks = _weights(2, 96, 256, 9, 90, 160)
+    blocks[:, ::3, 2, 1:] = 0
+    x = torch.randn(T, 256, generator=g) * torch.exp2(torch.randint(-30, 30, (T, 8, 1), generator=g).float()
+                                                      ).expand(T, 8, 32).reshape(T, 256)
+    x[1] = 0
+    x[0, 64:96] = 0
+    _check(blocks, x.cuda(), _ids(T, 2, 2, 3), "broadcast")
+
+
+@pytest.mark.parametrize("T", [2, 70])
+def test_nan_rows_stay_in_their_rows(T):
+    blocks = _weights(3, 50, 128, 11)
+    x = torch.randn(T, 128, generator=torch.Generator().manual_seed(12)).cuda()
+    x[1, 70] = float("nan")
+    ids = _ids(T, 2, 3, 4)
+    dst = _run(blocks, x, ids, "broadcast")
+    assert torch.isnan(dst[1]).all()
+    x[1] = 0
+    clean = _run(blocks, x, ids, "broadcast")
+    keep = [t for t in range(T) if t != 1]
+    assert torch.equal(dst[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [3, 80])
+def test_bad_id_is_reported(T):
+    blocks = _weights(4, 32, 64, 13)
+    x = torch.randn(T, 64, generator=torch.Generator().manual_seed(1)).cuda()
+    ids = _ids(T, 2, 4, 5)
+    for bad in (-1, 4, 2 ** 30):
+        b = ids.clone()
+        b[T - 1, 1] = bad
+        with pytest.raises(moe.MoeError) as e:
+            _run(blocks, x, b, "broadcast")
+        assert e.value.code == moe.ERR_BAD_ID
+    _check(blocks, x, ids, "broadcast")
+
+
+@pytest.mark.parametrize("T", [4, 200])
+def test_results_follow_the_rounded_values(T):
+    # the product of the rounded operands: mul_mat_id on the values that the quantiser returns
+    E, n_out, n_in, k = 8, 144, 320, 3
+    blocks = _weights(E, n_out, n_in, 15)
+    x = torch.randn(T, n_in, generator=torch.Generator().manual_seed(16)).bfloat16().cuda()
+    ids = _ids(T, k, E, 17)
+    dst = _run(blocks, x, ids, "broadcast")
+    _, values = moe.mxfp4_quantize(x, with_values=True)
+    W = moe.weights_prepare(blocks.cuda(), E, n_out, n_in, wtype="mxfp4")
+    other = moe.mul_mat_id(W, E, n_out, n_in, values, ids.cuda(), wtype="mxfp4")
+    _, mag = ref.mx_product(blocks.numpy(), x.double().cpu().numpy(), ids.numpy(), False)
+    assert (np.abs((dst - other).double().cpu().numpy()) <= 2 * n_in * 2.0 ** -23 * mag).all()
+
+
+@pytest.mark.parametrize("T", [4, 100])
+def test_graph_replay_rows_behind_and_two_workspaces(T):
+    E, n_out, n_in, k = 8, 100, 224, 2
+    blocks = _weights(E, n_out, n_in, 19)
+    W = moe.weights_prepare(blocks.cuda(), E, n_out, n_in, wtype="mxfp4")
+    g = torch.Generator().manual_seed(20)
+    x = torch.randn(T, n_in, generator=g).bfloat16().cuda()
+    ids = _ids(T, k, E, 21).cuda()
+    ws = moe.workspace(T, k, E, n_in)
+    out = torch.full((T + 2, k, n_out), -7.0).cuda()
+    moe.mul_mat_id_mx4(W, E, n_out, n_in, x, ids, ws=ws, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.mul_mat_id_mx4(W, E, n_out, n_in, x, ids, ws=ws, out=out)
+    x2 = torch.randn(T, n_in, generator=g).bfloat16().cuda()
+    ids2 = _ids(T, k, E, 22).cuda()
+    x.copy_(x2)
+    ids.copy_(ids2)
+    for _ in range(3):
+        graph.replay()
+    assert moe.get_status(ws) == moe.OK
+    assert (out[T:] == -7).all()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ws2 = moe.workspace(T, k, E, n_in)
+        other = moe.mul_mat_id_mx4(W, E, n_out, n_in, x2, ids2, ws=ws2)
+    side.synchronize()
+    assert torch.equal(out[:T], other)
+
+
+def test_no_tokens():
+    blocks = _weights(4, 32, 64, 23)
+    assert _run(blocks, torch.empty(0, 64).cuda(), torch.empty(0, 2, dtype=torch.int32), "broadcast").shape == (0, 2, 32)
+
+
+@pytest.mark.parametrize("T", [3, 90])
+def test_layer_forward_and_router_gradient(T):
+    # route_scored -> product of quantised experts -> combine, and back to the logits
+    E, n_in, n_out, k = 16, 128, 96, 4
+    g = torch.Generator().manual_seed(T)
+    blocks = moe.mxfp4_quantize(torch.randn(E, n_out, n_in, generator=g).cuda())
+    W = moe.weights_prepare(blocks, E, n_out, n_in, wtype="mxfp4")
+    x = torch.randn(T, n_in, generator=g).bfloat16().cuda()
+    logits = torch.randn(T, E, generator=g).cuda()
+    bias = (torch.randn(E, generator=g) * 0.05).cuda()
+    kw = dict(score="sigmoid", normalize=True, scale=2.5)
+    ids, w = moe.route_scored(logits, k, bias=bias, n_groups=4, topk_groups=2, group_score="top2", **kw)
+    dst = moe.mul_mat_id_mx4(W, E, n_out, n_in, x, ids)
+    y = moe.combine(dst, w)
+    dy = torch.randn(T, n_out, generator=g).cuda()
+    dw, ddst = moe.combine_backward(dy, dst, w)
+    dl = moe.route_scored_backward(logits, ids, dw, **kw)
+    # the 64-bit layer on the same choice
+    l = logits.double().cpu().numpy()
+    r_ids, r_w, _ = ref.route(l, k, bias.double().cpu().numpy(), "sigmoid", 4, 2, "top2", True, 2.5)
+    assert np.array_equal(ids.cpu().numpy(), r_ids)
+    r_dst, mag = ref.mx_product(blocks.cpu().numpy(), x.double().cpu().numpy(), r_ids, False)
+    r_y = np.einsum("tk,tkn->tn", r_w, r_dst)
+    r_dw, _, r_dd = ref.combine_grad(dy.cpu().numpy(), r_dst, r_w)
+    r_dl, _ = ref.route_grad(l, r_ids, r_dw, "sigmoid", True, 2.5, ref.U)
+    # every stage's bound is below 2^-15 of the magnitudes it sums
+    rel = 2.0 ** -15
+    assert (np.abs(y.double().cpu().numpy() - r_y) <= rel * np.einsum("tk,tkn->tn", r_w, mag)).all()
+    mag_dw = np.einsum("tn,tkn->tk", np.abs(dy.double().cpu().numpy()), mag)
+    assert (np.abs(dw.double().cpu().numpy() - r_dw) <= rel * mag_dw).all()
+    assert (np.abs(ddst.double().cpu().numpy() - r_dd) <= rel * np.abs(r_dd) + 1e-30).all()
+    assert (np.abs(dl.double().cpu().numpy() - r_dl) <= rel * 2.5 * 2 * mag_dw.max(1, keepdims=True)).all()
