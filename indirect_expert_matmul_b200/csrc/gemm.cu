@@ -43,6 +43,7 @@
 // word and every role leaves its loop.
 #include "common.cuh"
 #include "gemm_api.cuh"
+#include "bounded_wait.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -60,8 +61,6 @@ constexpr uint32_t kBTileBytes = kGemmBN * kTileK * 2; // 24 KB
 constexpr uint32_t kRawBytes = kTileM * kRowBytes;     // 8704
 constexpr int kSmemGroups = 256;                       // schedule tables kept in shared memory up to this
 constexpr int kPrefetchSteps = 8;                      // weight k-steps prefetched into L2 ahead of use
-constexpr long long kWaitLimitCycles = 1ll << 32;      // ~2 s
-constexpr uint32_t kSleepNs = 20000;                   // upper bound of one hardware wait
 // Tensor memory (512 columns): two fp32 accumulators of kGemmBN columns, then
 // kMA stages of the dequantised A operands, each two 128 x 64 matrices of
 // 16-bit values (32 columns a matrix: lane = row, two K values a column).
@@ -141,47 +140,6 @@ __device__ __forceinline__ Tile decode_tile(int t, int mt_count, const GemmParam
     r.p0pad = pad[lo] + j * kGemmBN;
     r.n = min(kGemmBN, bnd[lo + 1] - r.p0);
     return r;
-}
-
-// Bounded wait by one lane; false when the kernel is aborting.  The lane
-// sleeps in hardware between polls (suspend-time hint), so waiting roles do
-// not take issue slots from the dequantisation warps.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                         long long limit) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-        if (ptx::mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
-        if (*abort_flag) return false;
-        if (clock64() - t0 > limit) {
-            *abort_flag = 1;
-            const int site = (1 << 30) | ((int)(threadIdx.x >> 5) << 20) | (int)(ptx::smem_u32(bar) & 0xfffffu);
-            atomicCAS(status + (kHdrWaitSite - kHdrStatus), 0, site);
-            set_status(status, MOE_ERR_TIMEOUT);
-            return false;
-        }
-    }
-}
-
-// lane 0 waits, the warp learns the outcome
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                          long long limit) {
-    // every lane polls (no lane-0 branch); lanes that see different phases simply poll again
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (true) {
-        if (ptx::mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
-        if (*abort_flag) return false;
-        if (clock64() - t0 > limit) {
-            if ((threadIdx.x & 31) == 0) {
-                *abort_flag = 1;
-                const int site = (1 << 30) | ((int)(threadIdx.x >> 5) << 20) | (int)(ptx::smem_u32(bar) & 0xfffffu);
-                atomicCAS(status + (kHdrWaitSite - kHdrStatus), 0, site);
-                set_status(status, MOE_ERR_TIMEOUT);
-            }
-            return false;
-        }
-    }
 }
 
 // Operand type is a template parameter: a runtime choice inside the unrolled
@@ -926,14 +884,13 @@ static moe_status gather(const void* x, int x_type, int n_in, const int32_t* src
 
 moe_status launch_gemm_mul_mat_id(const GemmMulMatId& g, cudaStream_t stream) {
     const int mx = g.wtype == MOE_MXFP4;  // bf16 operands, unscaled activation rows
-    moe_status st = g.xt_ready ? MOE_OK
-                    : g.x_rows * g.k == g.S
+    moe_status st = g.x_rows * g.k == g.S
                         ? gather_tokens(g.x, g.x_type, g.n_in, g.slot_prow, g.k, g.x_rows, g.rows_pad, g.xt, g.xs,
                                         g.hdr, mx, stream)
                         : gather(g.x, g.x_type, g.n_in, g.ids_src1, g.bounds, g.pad_start, g.E, g.S, g.rows_pad, g.xt,
                                  g.xs, g.hdr, mx, stream);
     if (st) return st;
-    if (!g.xt_ready) prof_mark(stream, "gather");
+    prof_mark(stream, "gather");
     GemmParams p = {};
     p.A0 = g.W;
     p.L = WLayout(g.n_out, g.n_in, g.wtype);

@@ -24,7 +24,6 @@ struct GemmMulMatId {
     const int32_t* slot_prow;  // tiled row of each slot t*k+s
     int k;
     int* hdr;
-    int xt_ready;     // xt already holds the gathered rows as unscaled bf16: no gather
 };
 
 struct GemmFfn {

@@ -1,11 +1,28 @@
 // The indirect expert product with both operands in MXFP4:
 //   dst[t][s] = W[ids[t][s]] . Q(x[t] or x[t][s]),
 // Q rounding every 32 consecutive values to one E8M0 scale and E2M1 codes.
-// The gather rounds each row while it moves it to its expert's tile rows; the
-// rounded values are exact in bf16, so the grouped GEMM of bf16 operands gives
-// the product of the rounded operands.
-#include "gemm_api.cuh"
+//
+// Quantising gather: each row is rounded once and its codes go to the tile rows
+// of every slot that reads it: [K plane of 256 values][row][128 bytes], 16-byte
+// chunk c at c ^ (row % 8) (the 128-byte swizzle); the scales of 128 values of
+// a row are one word of [K / 128][row].
+//
+// Grouped GEMM (tcgen05 kind::mxf4, block scales): a CTA takes units of (up to
+// 192 sorted rows of one expert) x (one or two 128-row weight tiles) and streams
+// K in stages of 256 values.  The 4-bit weights go from their repacked form
+// straight to the tensor cores: the codes of a 32-row sub-block are 32 rows of
+// 32 bytes, which a tensor copy lays down in the 32-byte swizzle that the MMA
+// reads, so no thread touches them.  Four warps move the scales (1/17 of the
+// bytes) from shared to tensor memory, one thread issues the copies, one the
+// MMAs, and eight warps scatter the accumulators to dst.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "bounded_wait.cuh"
 #include "mxfp4.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -13,39 +30,449 @@ moe_status launch_row_ids(const int32_t* ids, int64_t S, int k, int E, int mode,
                           int32_t* ids_dst, int32_t* bounds, int32_t* active, int32_t* ntile_prefix,
                           int32_t* pad_start, int32_t* slot_prow, int bn, int* hdr, int32_t* rid_scratch,
                           cudaStream_t stream, int* launches = nullptr);
+bool testing_stall_state(int* cta, int* stage, long long* limit_cycles);
 
 namespace {
 
-// One warp per slot: eight values per lane, four lanes per block of 32.
+// ----------------------------------------------------------------- geometry
+constexpr int kMxThreads = 512;
+constexpr int kMxBN = kGemmBN;    // sorted rows (columns of the accumulator) of a unit
+constexpr int kMxStageKt = 4;     // 64-value k-steps of a stage
+constexpr int kMxStages = 3;
+constexpr uint32_t kMxCodes = kTileM * 32;                 // codes of a tile's k-step
+constexpr uint32_t kMxACodes = kMxStageKt * kMxCodes;      // 16384
+constexpr uint32_t kMxAScales = kMxStageKt * kTileM * 2;   // 1024
+constexpr uint32_t kMxB = kMxBN * 128;                     // 24576
+constexpr uint32_t kMxBScales = 2 * kMxBN * 4;             // 1536
+constexpr uint32_t kMxStageBytes = 2 * kMxACodes + kMxB + 2 * kMxAScales + kMxBScales;
+static_assert(kMxStageBytes % 1024 == 512, "stages are padded to the swizzle's 1024 bytes below");
+constexpr uint32_t kMxStagePitch = (kMxStageBytes + 1023) / 1024 * 1024;
+constexpr uint32_t kMxOffB = 2 * kMxACodes, kMxOffAS = kMxOffB + kMxB, kMxOffBS = kMxOffAS + 2 * kMxAScales;
+constexpr uint32_t kMxBarOff = kMxStages * kMxStagePitch;
+constexpr uint32_t kMxSmem = kMxBarOff + 256 + 1024;
+// tensor memory: two accumulators, then per stage 16 columns of A scales
+// (two tiles x two 128-value halves x four) and 16 of B scales (two halves x eight)
+constexpr uint32_t kMxScaleCol0 = 2 * kMxBN;
+static_assert(kMxScaleCol0 + kMxStages * 32 <= 512, "accumulators and scales fill tensor memory");
+constexpr int kMxSmemGroups = 256;
+
+struct Mx4Params {
+    CUtensorMap codes, scales;      // full 128-row tiles
+    CUtensorMap t_codes, r_codes;   // last tile: its 32-row sub-blocks, its 16-row sub-block
+    const uint8_t* W;
+    WLayout L;
+    int full_tiles;                 // tiles of 128 rows
+    int tail_subs, tail_r;          // last tile: number of 32-row sub-blocks, of 16-row ones (0 or 1)
+    int tiles_per_unit;             // 1 or 2
+    int n_groups;
+    const int32_t *bounds, *ntile_prefix, *pad_start;
+    const uint8_t* B;               // codes [plane][rows_pad][128]
+    const uint32_t* BS;             // scales [K / 128][scale_ld]
+    int64_t rows_pad, scale_ld;
+    const int32_t* dst_rows;
+    float* out;
+    int out_ld;
+    int* hdr;
+    long long wait_limit;
+    int stall_cta, stall_stage;     // test only: that CTA's activation copy of that stage is never issued (-1: off)
+};
+
+struct MxTile {
+    int e, mu, p0, n, p0pad;
+};
+
+__global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
+    extern __shared__ uint8_t smem_dyn[];
+    __shared__ int s_prefix[kMxSmemGroups + 1];
+    __shared__ int s_bounds[kMxSmemGroups + 1];
+    __shared__ int s_pad[kMxSmemGroups + 1];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+
+    if (read_status(p.hdr + kHdrStatus) != 0) return;
+
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_dyn + 1023) & ~(uintptr_t)1023);
+    uint64_t* full = (uint64_t*)(smem + kMxBarOff);  // a stage's copies have landed
+    uint64_t* sf_full = full + kMxStages;            // its scales are in tensor memory
+    uint64_t* empty = sf_full + kMxStages;           // its MMAs have completed
+    uint64_t* acc_full = empty + kMxStages;
+    uint64_t* acc_empty = acc_full + 1;
+    uint64_t* drained = acc_empty + 1;
+    volatile int* abort_flag = &s_abort;
+    int* status = p.hdr + kHdrStatus;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WLayout L = p.L;
+    const int MT = L.mt_count, KT = L.kt_count, KS = (KT + kMxStageKt - 1) / kMxStageKt;
+    const int TPU = p.tiles_per_unit, MU = (MT + TPU - 1) / TPU;
+    const bool in_smem = p.n_groups <= kMxSmemGroups;
+
+    if (tid == 0) {
+        for (int i = 0; i < kMxStages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&sf_full[i], 4);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        ptx::mbar_init(acc_full, 1);
+        ptx::mbar_init(acc_empty, 8);
+        ptx::mbar_init(drained, 1);
+        s_abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&s_tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    if (in_smem)
+        for (int i = tid; i <= p.n_groups; i += kMxThreads) {
+            s_prefix[i] = p.ntile_prefix[i];
+            s_bounds[i] = p.bounds[i];
+            s_pad[i] = p.pad_start[i];
+        }
+    const int total = p.hdr[kHdrTiles] * MU;
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    auto unit = [&](int t) {
+        MxTile r;
+        const int q = t / MU;
+        r.mu = t - q * MU;
+        const int* pre = in_smem ? s_prefix : p.ntile_prefix;
+        const int* bnd = in_smem ? s_bounds : p.bounds;
+        const int* pad = in_smem ? s_pad : p.pad_start;
+        int lo = 0, hi = p.n_groups;  // pre[lo] <= q < pre[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= q) lo = mid; else hi = mid;
+        }
+        r.e = lo;
+        const int j = q - pre[lo];
+        r.p0 = bnd[lo] + j * kMxBN;
+        r.p0pad = pad[lo] + j * kMxBN;
+        r.n = min(kMxBN, bnd[lo + 1] - r.p0);
+        return r;
+    };
+
+    // One k-step of the last, partial tile: its 32-row sub-blocks' codes in one
+    // tensor copy, its 16-row sub-block's in another, the scales by sub-block
+    // (a tensor copy's destination would need 128-byte alignment).
+    auto load_tail = [&](uint8_t* codes, uint8_t* scales, int e, int kt, uint64_t* bar) {
+        const uint8_t* src = p.W + L.block(e, MT - 1, kt);
+        if (p.tail_subs) ptx::tma_load_5d(codes, &p.t_codes, 0, 0, 0, kt, e, bar);
+        if (p.tail_r) ptx::tma_load_5d(codes + p.tail_subs * 1024, &p.r_codes, 0, 0, 0, kt, e, bar);
+        for (int sb = 0; sb < p.tail_subs; ++sb)
+            ptx::bulk_g2s(scales + sb * 64, src + sb * (kSubRows * kRowBytesMx) + kSubRows * 32, kSubRows * 2, bar);
+        if (p.tail_r)
+            ptx::bulk_g2s(scales + p.tail_subs * 64, src + p.tail_subs * (kSubRows * kRowBytesMx) + 16 * 32, 16 * 2,
+                          bar);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0) {
+            int s = 0, q = 0;
+            uint32_t ph = 0, used = 0, par = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const MxTile u = unit(t);
+                const uint32_t n16 = (uint32_t)(u.n + 15) & ~15u;
+                for (int ks = 0; ks < KS; ++ks, ++q) {
+                    ok = wait_bar(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
+                    if (!ok) break;
+                    uint8_t* st = smem + s * kMxStagePitch;
+                    const int kts = min(kMxStageKt, KT - ks * kMxStageKt), halves = (kts + 1) / 2;
+                    const bool stalled = (int)blockIdx.x == p.stall_cta && q == p.stall_stage;
+                    uint32_t bytes = n16 * 128u + halves * n16 * 4u;
+                    for (int i = 0; i < TPU; ++i) {
+                        const int mt = u.mu * TPU + i;
+                        if (mt < p.full_tiles) bytes += kMxACodes + kMxAScales;
+                        else if (mt < MT) bytes += (uint32_t)(kts * L.rows(mt) * kRowBytesMx);
+                    }
+                    if (!stalled) {
+                        ptx::mbar_arrive_expect_tx(&full[s], bytes);
+                        for (int i = 0; i < TPU; ++i) {
+                            const int mt = u.mu * TPU + i;
+                            uint8_t* ac = st + i * kMxACodes;
+                            uint8_t* as = st + kMxOffAS + i * kMxAScales;
+                            if (mt < p.full_tiles) {
+                                ptx::tma_load_5d(ac, &p.codes, 0, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
+                                ptx::tma_load_4d(as, &p.scales, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
+                            } else if (mt < MT) {
+                                for (int j = 0; j < kts; ++j)
+                                    load_tail(ac + j * kMxCodes, as + j * 256, u.e, ks * kMxStageKt + j, &full[s]);
+                            }
+                        }
+                        ptx::bulk_g2s(st + kMxOffB, p.B + ((size_t)ks * p.rows_pad + u.p0pad) * 128u, n16 * 128u,
+                                      &full[s]);
+                        for (int h = 0; h < halves; ++h)
+                            ptx::bulk_g2s(st + kMxOffBS + h * (kMxBN * 4),
+                                          p.BS + (size_t)(2 * ks + h) * p.scale_ld + u.p0pad, n16 * 4u, &full[s]);
+                        used |= 1u << s;
+                        par = (par & ~(1u << s)) | (ph << s);
+                    }
+                    if (++s == kMxStages) { s = 0; ph ^= 1; }
+                }
+            }
+            // let every copy issued land before the CTA can exit (bounded)
+            volatile int never = 0;
+            for (int i = 0; i < kMxStages; ++i)
+                if (used >> i & 1) wait_bar(&full[i], (par >> i) & 1, &never, status, p.wait_limit);
+        }
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMAs
+        int s = 0;
+        uint32_t ph = 0, use = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const MxTile u = unit(t);
+            const int n16 = (u.n + 15) & ~15;
+            const uint32_t id0 = ptx::idesc_mxf4(n16, 0), id1 = ptx::idesc_mxf4(n16, 1);
+            const int tiles = min(TPU, MT - u.mu * TPU);
+            ok = warp_wait(acc_empty, (use & 1) ^ 1, abort_flag, status, p.wait_limit);
+            if (!ok) break;
+            use += 1;
+            for (int ks = 0; ks < KS; ++ks) {
+                ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
+                     warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t st = ptx::smem_u32(smem + s * kMxStagePitch);
+                    const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)s * 32u;
+                    const int kts = min(kMxStageKt, KT - ks * kMxStageKt);
+                    for (int j = 0; j < kts; ++j) {
+                        const uint64_t bd = ptx::desc_k_sw128(st + kMxOffB + j * 32);
+                        const uint32_t id = j & 1 ? id1 : id0, h = (uint32_t)j >> 1, acc = (ks | j) != 0;
+                        for (int i = 0; i < tiles; ++i)
+                            ptx::mma_mxf4_ss(tmem + i * kMxBN, ptx::desc_k_sw32(st + i * kMxACodes + j * kMxCodes), bd,
+                                             id, sf + i * 8 + h * 4, sf + 16 + h * 8, acc);
+                    }
+                    ptx::mma_commit(&empty[s]);
+                }
+                __syncwarp();
+                if (++s == kMxStages) { s = 0; ph ^= 1; }
+            }
+            if (!ok) break;
+            if (lane == 0) ptx::mma_commit(acc_full);
+            __syncwarp();
+        }
+        // every MMA issued has completed before the CTA can release tensor memory
+        if (lane == 0) {
+            ptx::mma_commit(drained);
+            volatile int never = 0;
+            wait_bar(drained, 0, &never, status, p.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------- scales, per stage
+        // Every warp writes its quarter of the lanes with the same words: lane r
+        // holds rows r, 32 + r, ... of a tile (or of the sorted rows), one column each.
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        const uint32_t dst = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + kMxScaleCol0;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int ks = 0; ks < KS; ++ks) {
+                ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS) + lane * 2;
+                const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 4;
+                uint32_t v[32];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int sb = 0; sb < 4; ++sb) {
+                            const uint32_t a = as + i * kMxAScales + h * 512 + sb * 64;
+                            v[i * 8 + h * 4 + sb] = ptx::lds16(a) | ptx::lds16(a + 256) << 16;
+                        }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        v[16 + h * 8 + c] = c < kMxBN / 32 ? ptx::lds32(bs + h * (kMxBN * 4) + c * 128) : 0u;
+                ptx::tc_fence_after();
+                ptx::tmem_st_32x32b_x32(dst + (uint32_t)s * 32u, v);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&sf_full[s]);
+                if (++s == kMxStages) { s = 0; ph ^= 1; }
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------- epilogue
+        // Warps 8-11 drain the first tile's accumulator, 12-15 the second's.
+        const int wq = warp & 3, i = (warp - 8) >> 2;
+        uint32_t use = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+            const MxTile u = unit(t);
+            const int mt = u.mu * TPU + i;
+            const bool live = i < TPU && mt < MT;
+            int orow[kMxBN / 32];  // output rows of columns 32 c + lane
+#pragma unroll
+            for (int c = 0; c < kMxBN / 32; ++c)
+                orow[c] = live && 32 * c + lane < u.n ? __ldg(p.dst_rows + u.p0 + 32 * c + lane) : -1;
+            if (!warp_wait(acc_full, use & 1, abort_flag, status, p.wait_limit)) break;
+            use += 1;
+            ptx::tc_fence_after();
+            if (live) {
+                const int m = mt * kTileM + 32 * wq + lane;
+                const bool m_ok = m < L.n_out;
+                float* out = p.out + m;
+#pragma unroll
+                for (int c = 0; c < kMxBN / 32; ++c) {
+                    if (32 * c >= u.n) break;
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + i * kMxBN + 32 * c, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int r = __shfl_sync(0xffffffffu, orow[c], j);
+                        if (r >= 0 && m_ok) out[(int64_t)r * p.out_ld] = __uint_as_float(v[j]);
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(acc_empty);
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// -------------------------------------------------------- quantising gather
+// One warp per source row (broadcast: a token, whose codes go to the tile rows
+// of its k slots; per slot: one slot): eight values a lane, four lanes a block.
 __global__ void __launch_bounds__(256)
-mx4_gather_kernel(const void* __restrict__ x, int type, int n_in, int KT, const int32_t* __restrict__ slot_prow,
-                  int k, int per_slot, int64_t S, int64_t rows_pad, uint8_t* __restrict__ xt, const int* hdr) {
+mx4_gather_kernel(const void* __restrict__ x, int type, int n_in, const int32_t* __restrict__ slot_prow, int copies,
+                  int64_t n_rows, int64_t rows_pad, int64_t scale_ld, uint8_t* __restrict__ codes,
+                  uint32_t* __restrict__ scales, const int* hdr) {
     if (read_status(hdr + kHdrStatus) != 0) return;
     const int lane = threadIdx.x & 31;
     const int esz = type == MOE_F32 ? 4 : 2;
+    const int planes = (n_in + 255) / 256;
     const int64_t nw = (int64_t)gridDim.x * (blockDim.x / 32);
-    for (int64_t p = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); p < S; p += nw) {
-        const int64_t row = per_slot ? p : p / k;
-        const int prow = __ldg(slot_prow + p);
-        for (int s0 = 0; s0 < KT * 8; s0 += 32) {
-            const int seg = s0 + lane, col = seg * 8;
+    for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < n_rows; r += nw) {
+        const int32_t* pr = slot_prow + r * copies;
+        for (int kp = 0; kp < planes; ++kp) {
+            const int col = kp * 256 + lane * 8;
             float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (col < n_in) mx_load8<true>((const char*)x + (row * n_in + col) * esz, type, v);
+            if (col < n_in) mx_load8<true>((const char*)x + (r * n_in + col) * esz, type, v);
             const uint32_t X = mx_scale_byte(mx_block_bits(v, 0xffffffffu));
             const uint32_t w = X == 255u ? 0u : mx_codes8(v, mx_inv_scale(X));
-            mx_values8(w, mx_scale(X), v);
-            if (seg < KT * 8) {
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                    h[i] = *(const uint32_t*)&b;
-                }
-                *(uint4*)(xt + ((size_t)(seg >> 3) * rows_pad + prow) * 128u + (((seg & 7) ^ (prow & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
+            uint32_t sw = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
+            sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
+            sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
+            const bool sc = (lane & 15) == 0 && col < n_in;
+            uint8_t* plane = codes + (size_t)kp * rows_pad * 128u + (lane & 3) * 4;
+            uint32_t* sp = scales + (size_t)(2 * kp + (lane >> 4)) * scale_ld;
+            for (int j = 0; j < copies; ++j) {
+                const int prow = __ldg(pr + j);
+                *(uint32_t*)(plane + (size_t)prow * 128u + (((lane >> 2) ^ (prow & 7)) << 4)) = w;
+                if (sc) sp[prow] = sw;
             }
         }
     }
+}
+
+// ------------------------------------------------------------------- host
+int mx_sm_count() {
+    static std::atomic<int> cached[64];
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && (n = cached[dev].load()) > 0) return n;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (n <= 0) n = 148;
+    if (dev >= 0 && dev < 64) cached[dev].store(n);
+    return n;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 mx_encoder() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> cached{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = cached.load();
+    if (fn) return fn;
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
+    cached.store(fn);
+    return fn;
+}
+
+bool encode(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+    auto enc = mx_encoder();
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<uint8_t*>(base), dims, strides,
+                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The repacked MXFP4 form as tensors of bytes.  A 32-row sub-block of a k-step
+// is 1088 bytes: 32 rows of 32 code bytes, then 64 scale bytes; a full tile's
+// k-steps and sub-blocks follow one another, so they are one dimension.
+bool plan_weights(Mx4Params& p, int n_experts) {
+    const WLayout& L = p.L;
+    const cuuint64_t sub = kSubRows * kRowBytesMx, ex = (cuuint64_t)L.expert_bytes, KT = (cuuint64_t)L.kt_count;
+    p.full_tiles = L.n_out_pad / kTileM;
+    const int tail = L.n_out_pad % kTileM;
+    p.tail_subs = tail / kSubRows;
+    p.tail_r = tail % kSubRows != 0;
+    if (p.full_tiles) {
+        const cuuint64_t tile = kTileM * KT * kRowBytesMx;
+        const cuuint64_t cd[5] = {32, kSubRows, KT * 4, (cuuint64_t)p.full_tiles, (cuuint64_t)n_experts};
+        const cuuint64_t cs[4] = {32, sub, tile, ex};
+        const cuuint32_t cb[5] = {32, kSubRows, kMxStageKt * 4, 1, 1};
+        const cuuint64_t sd[4] = {64, KT * 4, (cuuint64_t)p.full_tiles, (cuuint64_t)n_experts};
+        const cuuint64_t ss[3] = {sub, tile, ex};
+        const cuuint32_t sb[4] = {64, kMxStageKt * 4, 1, 1};
+        if (!encode(&p.codes, p.W, 5, cd, cs, cb, CU_TENSOR_MAP_SWIZZLE_32B) ||
+            !encode(&p.scales, p.W + kSubRows * 32, 4, sd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return false;
+    }
+    const uint8_t* last = p.W + L.block(0, L.mt_count - 1, 0);
+    const cuuint64_t step = (cuuint64_t)tail * kRowBytesMx;
+    if (p.tail_subs) {
+        const cuuint64_t d[5] = {32, kSubRows, (cuuint64_t)p.tail_subs, KT, (cuuint64_t)n_experts};
+        const cuuint64_t s[4] = {32, sub, step, ex};
+        const cuuint32_t b[5] = {32, kSubRows, (cuuint32_t)p.tail_subs, 1, 1};
+        if (!encode(&p.t_codes, last, 5, d, s, b, CU_TENSOR_MAP_SWIZZLE_32B)) return false;
+    }
+    if (p.tail_r) {
+        const cuuint64_t d[5] = {32, 16, 1, KT, (cuuint64_t)n_experts};
+        const cuuint64_t s[4] = {32, step, step, ex};
+        const cuuint32_t b[5] = {32, 16, 1, 1, 1};
+        if (!encode(&p.r_codes, last + p.tail_subs * sub, 5, d, s, b, CU_TENSOR_MAP_SWIZZLE_32B)) return false;
+    }
+    return true;
+}
+
+moe_status launch_mx4_gemm(Mx4Params& p, int64_t max_coltiles, cudaStream_t stream) {
+    p.wait_limit = kWaitLimitCycles;
+    p.stall_cta = -1;
+    p.stall_stage = 0;
+    long long limit = 0;
+    if (testing_stall_state(&p.stall_cta, &p.stall_stage, &limit)) p.wait_limit = limit;
+    if (cudaFuncSetAttribute(mx4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMxSmem) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    const int64_t units = max_coltiles * ((p.L.mt_count + p.tiles_per_unit - 1) / p.tiles_per_unit);
+    const int sms = mx_sm_count();
+    const unsigned grid = (unsigned)(units < sms ? units : sms);
+    mx4_gemm_kernel<<<grid, kMxThreads, kMxSmem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -72,40 +499,46 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     WsLayout W(n_tokens, k, n_experts, n_in, 0, 0, x_type);
     char* ws = (char*)workspace;
     int* hdr = (int*)(ws + W.hdr);
+    Mx4Params p = {};
+    p.W = (const uint8_t*)W_prepared;
+    p.L = WLayout(n_out, n_in, MOE_MXFP4);
+    if (!plan_weights(p, n_experts)) return MOE_ERR_CUDA;
     prof_begin(s);
     int n_rid = 1;
     moe_status st = launch_row_ids(ids, S, k, n_experts, mode, (int32_t*)(ws + W.src1), (int32_t*)(ws + W.dst),
                                    (int32_t*)(ws + W.bounds), (int32_t*)(ws + W.active), (int32_t*)(ws + W.tiles),
-                                   (int32_t*)(ws + W.pad), (int32_t*)(ws + W.sprow), kGemmBN, hdr,
+                                   (int32_t*)(ws + W.pad), (int32_t*)(ws + W.sprow), kMxBN, hdr,
                                    n_experts <= kRidMaxE ? (int32_t*)(ws + W.rid) : nullptr, s, &n_rid);
     if (st) return st;
     prof_mark(s, "row_ids", n_rid);
-    const int KT = (n_in + kTileK - 1) / kTileK;
-    const int64_t blocks = (S + 7) / 8;
-    mx4_gather_kernel<<<(unsigned)(blocks < 148 * 8 ? blocks : 148 * 8), 256, 0, s>>>(
-        x, x_type, n_in, KT, (const int32_t*)(ws + W.sprow), k, mode == MOE_PER_SLOT, S, W.rows_pad,
-        (uint8_t*)(ws + W.xt), hdr);
+    // The rounded rows take the workspace of the 16-bit ones: 128 bytes per 256
+    // values and 4 per 128 where those take 128 per 64.  Only up to 64 values do
+    // the scales not fit behind the codes; there they take the rows' factors.
+    uint8_t* codes = (uint8_t*)(ws + W.xt);
+    uint32_t* scales = n_in <= kTileK ? (uint32_t*)(ws + W.xs)
+                                      : (uint32_t*)(codes + (size_t)((n_in + 255) / 256) * W.rows_pad * 128u);
+    const int64_t scale_ld = (W.rows_pad + 3) / 4 * 4;  // bulk copies start on 16 bytes
+    const int64_t rows = mode == MOE_BROADCAST ? n_tokens : S, blocks = (rows + 7) / 8;
+    const int64_t cap = (int64_t)mx_sm_count() * 8;
+    mx4_gather_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, s>>>(
+        x, x_type, n_in, (const int32_t*)(ws + W.sprow), mode == MOE_BROADCAST ? k : 1, rows, W.rows_pad, scale_ld,
+        codes, scales, hdr);
     if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     prof_mark(s, "gather");
-    GemmMulMatId g = {};
-    g.wtype = MOE_MXFP4;
-    g.W = (const uint8_t*)W_prepared;
-    g.E = n_experts;
-    g.n_out = n_out;
-    g.n_in = n_in;
-    g.xt = ws + W.xt;
-    g.xs = (float*)(ws + W.xs);
-    g.rows_pad = W.rows_pad;
-    g.pad_start = (const int32_t*)(ws + W.pad);
-    g.S = S;
-    g.dst = dst;
-    g.bounds = (const int32_t*)(ws + W.bounds);
-    g.ntile_prefix = (const int32_t*)(ws + W.tiles);
-    g.ids_src1 = (const int32_t*)(ws + W.src1);
-    g.ids_dst = (const int32_t*)(ws + W.dst);
-    g.slot_prow = (const int32_t*)(ws + W.sprow);
-    g.k = k;
-    g.hdr = hdr;
-    g.xt_ready = 1;
-    return launch_gemm_mul_mat_id(g, s);
+    p.tiles_per_unit = 2;
+    p.n_groups = n_experts;
+    p.bounds = (const int32_t*)(ws + W.bounds);
+    p.ntile_prefix = (const int32_t*)(ws + W.tiles);
+    p.pad_start = (const int32_t*)(ws + W.pad);
+    p.B = codes;
+    p.BS = scales;
+    p.rows_pad = W.rows_pad;
+    p.scale_ld = scale_ld;
+    p.dst_rows = (const int32_t*)(ws + W.dst);
+    p.out = dst;
+    p.out_ld = n_out;
+    p.hdr = hdr;
+    st = launch_mx4_gemm(p, (S + kMxBN - 1) / kMxBN + (S < n_experts ? S : n_experts), s);
+    prof_mark(s, "gemm");
+    return st;
 }

@@ -128,6 +128,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0,
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Four rows (row0..row3) of a 2-D tensor map, one box wide starting at column
 // col, into consecutive box-sized slots at dst (tile::gather4).
 __device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int col, int r0, int r1, int r2, int r3,
@@ -176,6 +185,19 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D(tmem) (+)= (A * scales) (B * scales)^T, kind::mxf4: both operands packed
+// E2M1 codes in shared memory, one E8M0 scale per 32 values of each row in
+// tensor memory (sfa, sfb; layout at idesc_mxf4), fp32 accumulation.  K = 64.
+__device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 // Arrive on `bar` once all previously issued tcgen05 async operations of this thread complete.
@@ -228,6 +250,36 @@ __device__ __forceinline__ uint64_t desc_k_sw128(uint32_t smem_addr) {
     d |= (uint64_t)(1024u >> 4) << 32;  // SBO
     d |= (uint64_t)1u << 46;            // version
     d |= (uint64_t)2u << 61;            // SWIZZLE_128B
+    return d;
+}
+
+// The same for rows of 32 bytes in the 32-byte swizzle: 8-row groups 256 bytes
+// apart, layout type 6 (SWIZZLE_32B).
+__device__ __forceinline__ uint64_t desc_k_sw32(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;           // LBO (unused for swizzled K-major)
+    d |= (uint64_t)(256u >> 4) << 32;  // SBO
+    d |= (uint64_t)1u << 46;           // version
+    d |= (uint64_t)6u << 61;           // SWIZZLE_32B
+    return d;
+}
+
+// Instruction descriptor of kind::mxf4 with one E8M0 scale per 32 values: both
+// operands E2M1 and K-major, fp32 accumulator, M = 128, N in [16, 256] step 16.
+// The scales of row r sit in tensor-memory lane r % 32 (repeated in the four
+// lane quarters), column r / 32 from the scale address on; a column word holds
+// the four scales of 128 values of K, and half = 0 / 1 picks the two bytes of
+// an instruction's 64 values.
+__host__ __device__ __forceinline__ uint32_t idesc_mxf4(int n, int half) {
+    uint32_t d = 0;
+    d |= (uint32_t)(2 * half) << 4;          // B scale bytes 0-1 or 2-3
+    d |= 1u << 7;                            // A format: E2M1
+    d |= 1u << 10;                           // B format: E2M1
+    d |= (uint32_t)((n >> 3) & 0x3F) << 17;  // N >> 3
+    d |= 1u << 23;                           // scales are E8M0
+    d |= 1u << 27;                           // M >> 7
+    d |= (uint32_t)(2 * half) << 29;         // A scale bytes
     return d;
 }
 
