@@ -10,9 +10,14 @@
 // Grouped GEMM (tcgen05 kind::mxf4, block scales): a CTA takes units of (up to
 // 192 sorted rows of one expert) x (one or two 128-row weight tiles) and streams
 // K in stages of 256 values.  The 4-bit weights go from their repacked form
-// straight to the tensor cores: the codes of a 32-row sub-block are 32 rows of
-// 32 bytes, which a tensor copy lays down in the 32-byte swizzle that the MMA
-// reads, so no thread touches them.  Four warps move the scales (1/17 of the
+// straight to the tensor cores, no thread touches them.  The codes of a 32-row
+// sub-block are 32 rows of 32 bytes, which the MMA reads in the 32-byte swizzle
+// (address bit 4 ^= bit 7).  Copied as such, in boxes 32 bytes wide, they kept
+// the copy engine busy for ~3.5 cycles a row (567 us for the 4096-token gate
+// product); copied as lines of 128 bytes in the 128-byte swizzle (bits 4-6 ^=
+// bits 7-9) bit 4 comes out the same and bits 5-6 only permute rows: row r of
+// the sub-block lands in row r ^ (r >> 3).  The scales and the epilogue follow
+// that order (perm_row).  Four warps move the scales (1/17 of the
 // bytes) from shared to tensor memory, one thread issues the copies, one the
 // MMAs, and eight warps scatter the accumulators to dst.
 #include <cuda.h>
@@ -77,6 +82,9 @@ struct Mx4Params {
     int stall_cta, stall_stage;     // test only: that CTA's activation copy of that stage is never issued (-1: off)
 };
 
+// The sub-block row that the 128-byte swizzle puts in place r (and back).
+__device__ __forceinline__ int perm_row(int r) { return r ^ (r >> 3); }
+
 struct MxTile {
     int e, mu, p0, n, p0pad;
 };
@@ -86,6 +94,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
     __shared__ int s_prefix[kMxSmemGroups + 1];
     __shared__ int s_bounds[kMxSmemGroups + 1];
     __shared__ int s_pad[kMxSmemGroups + 1];
+    __shared__ __align__(16) int s_rows[8][kMxBN];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
 
@@ -109,7 +118,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
 
     if (tid == 0) {
         for (int i = 0; i < kMxStages; ++i) {
-            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&full[i], 3);
             ptx::mbar_init(&sf_full[i], 4);
             ptx::mbar_init(&empty[i], 1);
         }
@@ -169,59 +178,70 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                           bar);
     };
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2 || warp == 3) {
         // ------------------------------------------------------------ copies
-        if (lane == 0) {
-            int s = 0, q = 0;
-            uint32_t ph = 0, used = 0, par = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const MxTile u = unit(t);
-                const uint32_t n16 = (uint32_t)(u.n + 15) & ~15u;
-                for (int ks = 0; ks < KS; ++ks, ++q) {
-                    ok = wait_bar(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
-                    if (!ok) break;
-                    uint8_t* st = smem + s * kMxStagePitch;
-                    const int kts = min(kMxStageKt, KT - ks * kMxStageKt), halves = (kts + 1) / 2;
+        // Warps 0 and 2: the codes and scales of the unit's first and second
+        // weight tile; warp 3: the rows' codes and scales.  One thread issuing all
+        // of a stage's copies needed ~1300 cycles for it, twice the MMAs' time.
+        const uint32_t issue = ptx::elect_one();
+        const int i = warp >> 1;  // weight tile of warps 0 and 2
+        int s = 0, q = 0;
+        uint32_t ph = 0, used = 0, par = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const MxTile u = unit(t);
+            const uint32_t n16 = (uint32_t)(u.n + 15) & ~15u;
+            const int mt = u.mu * TPU + i;
+            const uint8_t* bsrc = p.B + (size_t)u.p0pad * 128u;
+            const uint32_t* ssrc = p.BS + u.p0pad;
+            for (int ks = 0; ks < KS; ++ks, ++q) {
+                ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                uint8_t* st = smem + s * kMxStagePitch;
+                const int kts = min(kMxStageKt, KT - ks * kMxStageKt), halves = (kts + 1) / 2;
+                if (warp == 3) {
                     const bool stalled = (int)blockIdx.x == p.stall_cta && q == p.stall_stage;
-                    uint32_t bytes = n16 * 128u + halves * n16 * 4u;
-                    for (int i = 0; i < TPU; ++i) {
-                        const int mt = u.mu * TPU + i;
-                        if (mt < p.full_tiles) bytes += kMxACodes + kMxAScales;
-                        else if (mt < MT) bytes += (uint32_t)(kts * L.rows(mt) * kRowBytesMx);
+                    if (issue && !stalled) {
+                        ptx::mbar_arrive_expect_tx(&full[s], n16 * 128u + halves * n16 * 4u);
+                        ptx::bulk_g2s(st + kMxOffB, bsrc, n16 * 128u, &full[s]);
+                        ptx::bulk_g2s(st + kMxOffBS, ssrc, n16 * 4u, &full[s]);
+                        if (halves == 2)
+                            ptx::bulk_g2s(st + kMxOffBS + kMxBN * 4, ssrc + p.scale_ld, n16 * 4u, &full[s]);
                     }
+                    bsrc += (size_t)p.rows_pad * 128u;
+                    ssrc += 2 * p.scale_ld;
                     if (!stalled) {
-                        ptx::mbar_arrive_expect_tx(&full[s], bytes);
-                        for (int i = 0; i < TPU; ++i) {
-                            const int mt = u.mu * TPU + i;
-                            uint8_t* ac = st + i * kMxACodes;
-                            uint8_t* as = st + kMxOffAS + i * kMxAScales;
-                            if (mt < p.full_tiles) {
-                                ptx::tma_load_5d(ac, &p.codes, 0, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
-                                ptx::tma_load_4d(as, &p.scales, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
-                            } else if (mt < MT) {
-                                for (int j = 0; j < kts; ++j)
-                                    load_tail(ac + j * kMxCodes, as + j * 256, u.e, ks * kMxStageKt + j, &full[s]);
-                            }
-                        }
-                        ptx::bulk_g2s(st + kMxOffB, p.B + ((size_t)ks * p.rows_pad + u.p0pad) * 128u, n16 * 128u,
-                                      &full[s]);
-                        for (int h = 0; h < halves; ++h)
-                            ptx::bulk_g2s(st + kMxOffBS + h * (kMxBN * 4),
-                                          p.BS + (size_t)(2 * ks + h) * p.scale_ld + u.p0pad, n16 * 4u, &full[s]);
                         used |= 1u << s;
                         par = (par & ~(1u << s)) | (ph << s);
                     }
-                    if (++s == kMxStages) { s = 0; ph ^= 1; }
+                } else if (issue) {
+                    uint8_t* ac = st + i * kMxACodes;
+                    uint8_t* as = st + kMxOffAS + i * kMxAScales;
+                    if (i < TPU && mt < p.full_tiles) {
+                        ptx::mbar_arrive_expect_tx(&full[s], kMxACodes + kMxAScales);
+                        ptx::tma_load_5d(ac, &p.codes, 0, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
+                        ptx::tma_load_4d(as, &p.scales, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
+                    } else if (i < TPU && mt < MT) {
+                        ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)(kts * L.rows(mt) * kRowBytesMx));
+                        for (int j = 0; j < kts; ++j)
+                            load_tail(ac + j * kMxCodes, as + j * 256, u.e, ks * kMxStageKt + j, &full[s]);
+                    } else {
+                        ptx::mbar_arrive(&full[s]);
+                    }
                 }
+                if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
-            // let every copy issued land before the CTA can exit (bounded)
+        }
+        // let every copy issued land before the CTA can exit (bounded): a stage
+        // completes when all three warps' copies have
+        if (warp == 3) {
             volatile int never = 0;
-            for (int i = 0; i < kMxStages; ++i)
-                if (used >> i & 1) wait_bar(&full[i], (par >> i) & 1, &never, status, p.wait_limit);
+            for (int j = 0; j < kMxStages; ++j)
+                if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, p.wait_limit);
         }
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMAs
+        const uint32_t issue = ptx::elect_one(), smem_a = ptx::smem_u32(smem);
         int s = 0;
         uint32_t ph = 0, use = 0;
         bool ok = true;
@@ -229,7 +249,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
             const MxTile u = unit(t);
             const int n16 = (u.n + 15) & ~15;
             const uint32_t id0 = ptx::idesc_mxf4(n16, 0), id1 = ptx::idesc_mxf4(n16, 1);
-            const int tiles = min(TPU, MT - u.mu * TPU);
+            const bool two = TPU == 2 && u.mu * 2 + 1 < MT;
             ok = warp_wait(acc_empty, (use & 1) ^ 1, abort_flag, status, p.wait_limit);
             if (!ok) break;
             use += 1;
@@ -238,28 +258,31 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                      warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t st = ptx::smem_u32(smem + s * kMxStagePitch);
-                    const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)s * 32u;
-                    const int kts = min(kMxStageKt, KT - ks * kMxStageKt);
-                    for (int j = 0; j < kts; ++j) {
-                        const uint64_t bd = ptx::desc_k_sw128(st + kMxOffB + j * 32);
-                        const uint32_t id = j & 1 ? id1 : id0, h = (uint32_t)j >> 1, acc = (ks | j) != 0;
-                        for (int i = 0; i < tiles; ++i)
-                            ptx::mma_mxf4_ss(tmem + i * kMxBN, ptx::desc_k_sw32(st + i * kMxACodes + j * kMxCodes), bd,
-                                             id, sf + i * 8 + h * 4, sf + 16 + h * 8, acc);
+                const uint32_t st = smem_a + (uint32_t)s * kMxStagePitch;
+                const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)s * 32u;
+                const uint64_t ad = ptx::desc_k_sw32(st), bd = ptx::desc_k_sw128(st + kMxOffB);
+                const int kts = KT - ks * kMxStageKt;
+#pragma unroll
+                for (int j = 0; j < kMxStageKt; ++j) {
+                    if (j < kts) {  // address fields count 16 bytes; sums stay inside their 14 bits
+                        const uint32_t id = j & 1 ? id1 : id0;
+                        ptx::mma_mxf4_ss(tmem, ad + (j * kMxCodes >> 4), bd + j * 2, id, sf + (j >> 1) * 4,
+                                         sf + 16 + (j >> 1) * 8, (ks | j) != 0, issue);
+                        if (two)
+                            ptx::mma_mxf4_ss(tmem + kMxBN, ad + ((kMxACodes + j * kMxCodes) >> 4), bd + j * 2, id,
+                                             sf + 8 + (j >> 1) * 4, sf + 16 + (j >> 1) * 8, (ks | j) != 0, issue);
                     }
-                    ptx::mma_commit(&empty[s]);
                 }
+                if (issue) ptx::mma_commit(&empty[s]);
                 __syncwarp();
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
             if (!ok) break;
-            if (lane == 0) ptx::mma_commit(acc_full);
+            if (issue) ptx::mma_commit(acc_full);
             __syncwarp();
         }
         // every MMA issued has completed before the CTA can release tensor memory
-        if (lane == 0) {
+        if (issue) {
             ptx::mma_commit(drained);
             volatile int never = 0;
             wait_bar(drained, 0, &never, status, p.wait_limit);
@@ -277,7 +300,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
             for (int ks = 0; ks < KS; ++ks) {
                 ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
-                const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS) + lane * 2;
+                const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS) + perm_row(lane) * 2;
                 const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 4;
                 uint32_t v[32];
 #pragma unroll
@@ -307,34 +330,46 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         // ---------------------------------------------------------- epilogue
         // Warps 8-11 drain the first tile's accumulator, 12-15 the second's.
         const int wq = warp & 3, i = (warp - 8) >> 2;
+        int* rows = s_rows[warp - 8];  // the warp's copy of the unit's output rows
         uint32_t use = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x) {
             const MxTile u = unit(t);
             const int mt = u.mu * TPU + i;
             const bool live = i < TPU && mt < MT;
-            int orow[kMxBN / 32];  // output rows of columns 32 c + lane
-#pragma unroll
-            for (int c = 0; c < kMxBN / 32; ++c)
-                orow[c] = live && 32 * c + lane < u.n ? __ldg(p.dst_rows + u.p0 + 32 * c + lane) : -1;
+            __syncwarp();
+            for (int c = lane; c < u.n; c += 32) rows[c] = __ldg(p.dst_rows + u.p0 + c);
+            __syncwarp();
             if (!warp_wait(acc_full, use & 1, abort_flag, status, p.wait_limit)) break;
             use += 1;
             ptx::tc_fence_after();
             if (live) {
-                const int m = mt * kTileM + 32 * wq + lane;
+                const int m = mt * kTileM + 32 * wq + perm_row(lane);
                 const bool m_ok = m < L.n_out;
                 float* out = p.out + m;
-#pragma unroll
-                for (int c = 0; c < kMxBN / 32; ++c) {
-                    if (32 * c >= u.n) break;
+                // A column is a sorted row: its 32 lanes are 128 consecutive bytes of one
+                // row of dst.  The rows' numbers come from shared memory, four to a load: by
+                // shuffles under a test a column cost 105 cycles (20000 a unit) against ~25.
+                for (int c0 = 0; c0 < u.n; c0 += 32) {
                     uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + i * kMxBN + 32 * c, v);
+                    ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + i * kMxBN + c0, v);
                     ptx::tmem_ld_wait();
+                    if (!m_ok) continue;
+                    if (c0 + 32 <= u.n) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int r = __shfl_sync(0xffffffffu, orow[c], j);
-                        if (r >= 0 && m_ok) out[(int64_t)r * p.out_ld] = __uint_as_float(v[j]);
+                        for (int j = 0; j < 32; j += 4) {
+                            const int4 r = *(const int4*)(rows + c0 + j);
+                            out[(int64_t)r.x * p.out_ld] = __uint_as_float(v[j]);
+                            out[(int64_t)r.y * p.out_ld] = __uint_as_float(v[j + 1]);
+                            out[(int64_t)r.z * p.out_ld] = __uint_as_float(v[j + 2]);
+                            out[(int64_t)r.w * p.out_ld] = __uint_as_float(v[j + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c0 + j < u.n) out[(int64_t)rows[c0 + j] * p.out_ld] = __uint_as_float(v[j]);
                     }
                 }
+                __syncwarp();
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -421,8 +456,9 @@ bool encode(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_t* dim
 }
 
 // The repacked MXFP4 form as tensors of bytes.  A 32-row sub-block of a k-step
-// is 1088 bytes: 32 rows of 32 code bytes, then 64 scale bytes; a full tile's
-// k-steps and sub-blocks follow one another, so they are one dimension.
+// is 1088 bytes: 32 rows of 32 code bytes (eight lines of 128), then 64 scale
+// bytes; a full tile's k-steps and sub-blocks follow one another, so they are
+// one dimension.
 bool plan_weights(Mx4Params& p, int n_experts) {
     const WLayout& L = p.L;
     const cuuint64_t sub = kSubRows * kRowBytesMx, ex = (cuuint64_t)L.expert_bytes, KT = (cuuint64_t)L.kt_count;
@@ -432,29 +468,29 @@ bool plan_weights(Mx4Params& p, int n_experts) {
     p.tail_r = tail % kSubRows != 0;
     if (p.full_tiles) {
         const cuuint64_t tile = kTileM * KT * kRowBytesMx;
-        const cuuint64_t cd[5] = {32, kSubRows, KT * 4, (cuuint64_t)p.full_tiles, (cuuint64_t)n_experts};
-        const cuuint64_t cs[4] = {32, sub, tile, ex};
-        const cuuint32_t cb[5] = {32, kSubRows, kMxStageKt * 4, 1, 1};
+        const cuuint64_t cd[5] = {128, 8, KT * 4, (cuuint64_t)p.full_tiles, (cuuint64_t)n_experts};
+        const cuuint64_t cs[4] = {128, sub, tile, ex};
+        const cuuint32_t cb[5] = {128, 8, kMxStageKt * 4, 1, 1};
         const cuuint64_t sd[4] = {64, KT * 4, (cuuint64_t)p.full_tiles, (cuuint64_t)n_experts};
         const cuuint64_t ss[3] = {sub, tile, ex};
         const cuuint32_t sb[4] = {64, kMxStageKt * 4, 1, 1};
-        if (!encode(&p.codes, p.W, 5, cd, cs, cb, CU_TENSOR_MAP_SWIZZLE_32B) ||
+        if (!encode(&p.codes, p.W, 5, cd, cs, cb, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !encode(&p.scales, p.W + kSubRows * 32, 4, sd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE))
             return false;
     }
     const uint8_t* last = p.W + L.block(0, L.mt_count - 1, 0);
     const cuuint64_t step = (cuuint64_t)tail * kRowBytesMx;
     if (p.tail_subs) {
-        const cuuint64_t d[5] = {32, kSubRows, (cuuint64_t)p.tail_subs, KT, (cuuint64_t)n_experts};
-        const cuuint64_t s[4] = {32, sub, step, ex};
-        const cuuint32_t b[5] = {32, kSubRows, (cuuint32_t)p.tail_subs, 1, 1};
-        if (!encode(&p.t_codes, last, 5, d, s, b, CU_TENSOR_MAP_SWIZZLE_32B)) return false;
+        const cuuint64_t d[5] = {128, 8, (cuuint64_t)p.tail_subs, KT, (cuuint64_t)n_experts};
+        const cuuint64_t s[4] = {128, sub, step, ex};
+        const cuuint32_t b[5] = {128, 8, (cuuint32_t)p.tail_subs, 1, 1};
+        if (!encode(&p.t_codes, last, 5, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
     }
     if (p.tail_r) {
-        const cuuint64_t d[5] = {32, 16, 1, KT, (cuuint64_t)n_experts};
-        const cuuint64_t s[4] = {32, step, step, ex};
-        const cuuint32_t b[5] = {32, 16, 1, 1, 1};
-        if (!encode(&p.r_codes, last + p.tail_subs * sub, 5, d, s, b, CU_TENSOR_MAP_SWIZZLE_32B)) return false;
+        const cuuint64_t d[5] = {128, 4, 1, KT, (cuuint64_t)n_experts};
+        const cuuint64_t s[4] = {128, step, step, ex};
+        const cuuint32_t b[5] = {128, 4, 1, 1, 1};
+        if (!encode(&p.r_codes, last + p.tail_subs * sub, 5, d, s, b, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
     }
     return true;
 }
