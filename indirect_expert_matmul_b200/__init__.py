@@ -152,14 +152,20 @@ def _need(t, name, dtype, numel, device=None):
     return t
 
 
+# the current stream's handle by device index (the Stream object costs 2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _call(what, dev, fn, *args):
     """Run an entry point with `dev` current and its current stream as the last
     argument (a launch needs its stream's device to be the current one)."""
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    i = dev.index
+    if i == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _raw_stream(i))
     if rc != OK:
         raise MoeError(rc, what)
 
