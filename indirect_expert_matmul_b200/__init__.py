@@ -170,19 +170,28 @@ def _call(what, dev, fn, *args):
         raise MoeError(rc, what)
 
 
+def _at(t, name, dtype, numel, dev):
+    """The address of a tensor that _need accepts (the checks in one test: a
+    small call's time is the host's)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.is_contiguous() \
+            and t.numel() >= numel:
+        return t.data_ptr()
+    return _need(t, name, dtype, numel, dev).data_ptr()
+
+
 def _rows(t, name):
     """(n_rows, n, row stride) of a CUDA tensor whose last dimension has no
     gaps: contiguous, or two-dimensional with rows a fixed stride apart."""
     _gpu(t, name)
-    if t.dim() < 1:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    n = t.shape[-1]
-    rows = t.numel() // n if n else 0
+    n = shape[-1]
     if t.is_contiguous():
-        return rows, n, max(n, 1)
-    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < n:
+        return (shape[0] if len(shape) == 2 else t.numel() // n if n else 0), n, n or 1
+    if len(shape) != 2 or t.stride(1) != 1 or t.stride(0) < n:
         raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
-    return rows, n, t.stride(0) if rows > 1 else n
+    return shape[0], n, t.stride(0) if shape[0] > 1 else n
 
 
 # ----------------------------------------------------------------- memory
@@ -239,16 +248,14 @@ def mxfp4_quantize(x, with_values=False, out=None, values=None):
     if n % 32 or n == 0:
         raise ValueError("the last dimension of x must be a positive multiple of 32")
     dev = x.device
-    shape = tuple(x.shape)
+    shape = x.shape
     if out is None:
         out = torch.empty(shape[:-1] + (n // 32, 17), dtype=torch.uint8, device=dev)
-    _need(out, "out", torch.uint8, rows * (n // 32) * 17, dev)
     if values is None and with_values:
         values = torch.empty(shape, dtype=x.dtype, device=dev)
-    if values is not None:
-        _need(values, "values", x.dtype, rows * n, dev)
     _call("moe_mxfp4_quantize", dev, _L().moe_mxfp4_quantize, x.data_ptr(), _XTYPE[x.dtype], ld, rows, n,
-          out.data_ptr(), None if values is None else values.data_ptr())
+          _at(out, "out", torch.uint8, rows * (n // 32) * 17, dev),
+          None if values is None else _at(values, "values", x.dtype, rows * n, dev))
     return out if values is None else (out, values)
 
 
@@ -310,17 +317,17 @@ def mul_mat_id_mx4(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None,
     dev = x.device
     _cuda(ids, "ids", torch.int32, dev)
     T, k = ids.shape
-    _need(W, "W", torch.uint8, weights_prepared_size(n_experts, n_out, n_in, MXFP4), dev)
-    _need(x, "x", x.dtype, (T if _MODE[mode] == BROADCAST else T * k) * n_in)
+    xt, m, L = _XTYPE[x.dtype], _MODE[mode], _L()
     own_ws = ws is None
     if own_ws:
         ws = workspace(T, k, n_experts, n_in, x_dtype=x.dtype, device=dev)
-    _need(ws, "ws", torch.uint8, workspace_size(T, k, n_experts, n_in, x_dtype=x.dtype), dev)
     if out is None:
         out = torch.empty((T, k, n_out), dtype=torch.float32, device=dev)
-    _need(out, "out", torch.float32, T * k * n_out, dev)
-    _call("moe_mul_mat_id_mx4", dev, _L().moe_mul_mat_id_mx4, W.data_ptr(), n_experts, n_out, n_in, x.data_ptr(),
-          _XTYPE[x.dtype], ids.data_ptr(), T, k, _MODE[mode], out.data_ptr(), ws.data_ptr())
+    _call("moe_mul_mat_id_mx4", dev, L.moe_mul_mat_id_mx4,
+          _at(W, "W", torch.uint8, L.moe_weights_prepared_size_w(MXFP4, n_experts, n_out, n_in), dev),
+          n_experts, n_out, n_in, _at(x, "x", x.dtype, (T if m == BROADCAST else T * k) * n_in, dev), xt,
+          ids.data_ptr(), T, k, m, _at(out, "out", torch.float32, T * k * n_out, dev),
+          _at(ws, "ws", torch.uint8, L.moe_workspace_size(T, k, n_experts, n_in, 0, 0, xt), dev))
     if own_ws:
         _chk(get_status(ws), "moe_mul_mat_id_mx4 (device status)")
     return out
@@ -435,17 +442,14 @@ def route_scored(logits, k, bias=None, score="sigmoid", n_groups=1, topk_groups=
         raise ValueError("logits must be a [T][E] tensor of float32, bfloat16 or float16")
     T, E, ld = _rows(logits, "logits")
     dev = logits.device
-    if bias is not None:
-        _need(bias, "bias", torch.float32, E, dev)
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _need(ids, "ids", torch.int32, T * k, dev)
-    _need(weights, "weights", torch.float32, T * k, dev)
     _call("moe_route_scored", dev, _L().moe_route_scored, logits.data_ptr(), _XTYPE[logits.dtype], ld,
-          None if bias is None else bias.data_ptr(), T, E, k, _SCORE[score], n_groups, topk_groups,
-          _GROUP_TOP[group_score], 1 if normalize else 0, scale, ids.data_ptr(), weights.data_ptr())
+          None if bias is None else _at(bias, "bias", torch.float32, E, dev), T, E, k, _SCORE[score], n_groups,
+          topk_groups, _GROUP_TOP[group_score], 1 if normalize else 0, scale,
+          _at(ids, "ids", torch.int32, T * k, dev), _at(weights, "weights", torch.float32, T * k, dev))
     return ids, weights
 
 
@@ -462,13 +466,11 @@ def route_scored_backward(logits, ids, dweights, score="sigmoid", normalize=True
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError("ids must be [T][k]")
     k = ids.shape[1]
-    _need(dweights, "dweights", torch.float32, T * k, dev)
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    _need(out, "out", logits.dtype, T * E, dev)
     _call("moe_route_scored_backward", dev, _L().moe_route_scored_backward, logits.data_ptr(), _XTYPE[logits.dtype],
-          ld, ids.data_ptr(), dweights.data_ptr(), T, E, k, _SCORE[score], 1 if normalize else 0, scale,
-          out.data_ptr())
+          ld, ids.data_ptr(), _at(dweights, "dweights", torch.float32, T * k, dev), T, E, k, _SCORE[score],
+          1 if normalize else 0, scale, _at(out, "out", logits.dtype, T * E, dev))
     return out
 
 
@@ -486,18 +488,15 @@ def combine_backward(dy, dst, weights, need_ddst=True, dweights=None, ddst=None)
     n = dst.shape[-1]
     if dst.numel() != T * k * n:
         raise ValueError("dst must hold n_tokens*k rows of n")
-    _need(dy, "dy", torch.float32, T * n, dev)
     if dweights is None:
         dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    _need(dweights, "dweights", torch.float32, T * k, dev)
     if not need_ddst:
         ddst = None
     elif ddst is None:
         ddst = torch.empty_like(dst)
-    if ddst is not None:
-        _need(ddst, "ddst", torch.float32, T * k * n, dev)
-    _call("moe_combine_backward", dev, _L().moe_combine_backward, dy.data_ptr(), dst.data_ptr(), weights.data_ptr(),
-          T, k, n, dweights.data_ptr(), None if ddst is None else ddst.data_ptr())
+    _call("moe_combine_backward", dev, _L().moe_combine_backward, _at(dy, "dy", torch.float32, T * n, dev),
+          dst.data_ptr(), weights.data_ptr(), T, k, n, _at(dweights, "dweights", torch.float32, T * k, dev),
+          None if ddst is None else _at(ddst, "ddst", torch.float32, T * k * n, dev))
     return dweights, ddst
 
 
