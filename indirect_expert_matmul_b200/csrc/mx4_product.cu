@@ -28,6 +28,7 @@
 #include "bounded_wait.cuh"
 #include "mxfp4.cuh"
 #include "ptx.cuh"
+#include "warp_match.cuh"
 
 namespace moe {
 
@@ -96,9 +97,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
     __shared__ int s_pad[kMxSmemGroups + 1];
     __shared__ __align__(16) int s_rows[8][kMxBN];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
-
-    if (read_status(p.hdr + kHdrStatus) != 0) return;
+    __shared__ int s_abort, s_total;
 
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_dyn + 1023) & ~(uintptr_t)1023);
     uint64_t* full = (uint64_t*)(smem + kMxBarOff);  // a stage's copies have landed
@@ -132,13 +131,18 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         ptx::tmem_alloc(&s_tmem, 512);
         ptx::tmem_relinquish();
     }
-    if (in_smem)
+    // (a programmatic dependent of the gather: nothing it wrote is read before it has ended)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (all threads by one thread's reading: another CTA may set the status meanwhile)
+    if (tid == 0) s_total = read_status(status) != 0 ? 0 : p.hdr[kHdrTiles] * MU;
+    __syncthreads();
+    const int total = s_total;
+    if (in_smem && total > 0)
         for (int i = tid; i <= p.n_groups; i += kMxThreads) {
             s_prefix[i] = p.ntile_prefix[i];
             s_bounds[i] = p.bounds[i];
             s_pad[i] = p.pad_start[i];
         }
-    const int total = p.hdr[kHdrTiles] * MU;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -386,36 +390,313 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
 }
 
 // -------------------------------------------------------- quantising gather
-// One warp per source row (broadcast: a token, whose codes go to the tile rows
-// of its k slots; per slot: one slot): eight values a lane, four lanes a block.
+// Where the rounded rows go: codes [plane of 256 values][row][128 bytes], the
+// 16-byte chunk of block c at c ^ (row % 8); scales [128 values][row], a word
+// of four scale bytes.
+struct MxRows {
+    uint8_t* codes;
+    uint32_t* scales;
+    int64_t rows_pad, scale_ld;
+};
+
+// Eight consecutive values as they lie in memory: maximum and codes.
+template <int TYPE>
+struct MxEight {
+    uint32_t w[TYPE == MOE_F32 ? 8 : 4];
+
+    __device__ __forceinline__ void load(const void* p) {
+        const uint4 a = __ldg((const uint4*)p);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        if constexpr (TYPE == MOE_F32) {
+            const uint4 b = __ldg((const uint4*)p + 1);
+            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (TYPE == MOE_F32 ? 8 : 4); ++i) w[i] = 0u;
+    }
+    // the largest magnitude's bits as a float's (16-bit types: two at a time)
+    __device__ __forceinline__ uint32_t amax_bits() const {
+        uint32_t m = 0u;
+        if constexpr (TYPE == MOE_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+            m = max(m >> 16, m & 0xffffu);
+            return TYPE == MOE_BF16 ? m << 16 : __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+        }
+    }
+    __device__ __forceinline__ uint32_t codes(float inv) const {
+        float v[8];
+        if constexpr (TYPE == MOE_F32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (TYPE == MOE_BF16) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*(const __half2*)&w[i]);
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
+            }
+        }
+        return mx_codes8(v, inv);
+    }
+};
+
+constexpr int kMxPlanes = 4;  // planes of a row a warp has in flight
+
+// Planes kp0 .. kp0 + 3 (256 values each) of source row r by one warp, eight
+// values a lane, four lanes a block, to the tile rows prow[0 .. copies).
+template <int TYPE>
+__device__ __forceinline__ void round_planes(const void* __restrict__ x, int64_t r, int n_in, int kp0, int planes,
+                                             const int32_t* prow, int copies, const MxRows& o, int lane) {
+    constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
+    const int col = kp0 * 256 + lane * 8;
+    const char* src = (const char*)x + (r * n_in + col) * esz;
+    MxEight<TYPE> v[kMxPlanes];
+#pragma unroll
+    for (int i = 0; i < kMxPlanes; ++i) {
+        if (col + i * 256 < n_in) v[i].load(src + i * 256 * esz);
+        else v[i].zero();
+    }
+    uint32_t w[kMxPlanes], sw[kMxPlanes];
+#pragma unroll
+    for (int i = 0; i < kMxPlanes; ++i) {
+        uint32_t m = v[i].amax_bits();
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t X = mx_scale_byte(m);
+        w[i] = X == 255u ? 0u : v[i].codes(mx_inv_scale(X));
+        sw[i] = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
+        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 4);
+        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 8);
+    }
+    const size_t pitch = (size_t)o.rows_pad * 128u;
+    uint8_t* plane = o.codes + (size_t)kp0 * pitch + (lane & 3) * 4;
+    uint32_t* sp = o.scales + (size_t)(2 * kp0 + (lane >> 4)) * o.scale_ld;
+    const bool sc = (lane & 15) == 0;
+    for (int j = 0; j < copies; ++j) {
+        const uint32_t pr = (uint32_t)prow[j];
+        uint8_t* c = plane + ((size_t)pr * 128u + (((uint32_t)(lane >> 2) ^ (pr & 7u)) << 4));
+        uint32_t* q = sp + pr;
+#pragma unroll
+        for (int i = 0; i < kMxPlanes; ++i) {
+            if (kp0 + i < planes) *(uint32_t*)c = w[i];
+            if (sc && col + i * 256 < n_in) *q = sw[i];
+            c += pitch;
+            q += 2 * o.scale_ld;
+        }
+    }
+}
+
+// After the general row-id pass: one warp per source row (broadcast: a token,
+// whose codes go to the tile rows of its k slots; per slot: one slot).
+template <int TYPE>
 __global__ void __launch_bounds__(256)
-mx4_gather_kernel(const void* __restrict__ x, int type, int n_in, const int32_t* __restrict__ slot_prow, int copies,
-                  int64_t n_rows, int64_t rows_pad, int64_t scale_ld, uint8_t* __restrict__ codes,
-                  uint32_t* __restrict__ scales, const int* hdr) {
+mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restrict__ slot_prow, int copies,
+                  int64_t n_rows, MxRows o, const int* hdr) {
     if (read_status(hdr + kHdrStatus) != 0) return;
     const int lane = threadIdx.x & 31;
-    const int esz = type == MOE_F32 ? 4 : 2;
     const int planes = (n_in + 255) / 256;
     const int64_t nw = (int64_t)gridDim.x * (blockDim.x / 32);
-    for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < n_rows; r += nw) {
-        const int32_t* pr = slot_prow + r * copies;
-        for (int kp = 0; kp < planes; ++kp) {
-            const int col = kp * 256 + lane * 8;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (col < n_in) mx_load8<true>((const char*)x + (r * n_in + col) * esz, type, v);
-            const uint32_t X = mx_scale_byte(mx_block_bits(v, 0xffffffffu));
-            const uint32_t w = X == 255u ? 0u : mx_codes8(v, mx_inv_scale(X));
-            uint32_t sw = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
-            sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
-            sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
-            const bool sc = (lane & 15) == 0 && col < n_in;
-            uint8_t* plane = codes + (size_t)kp * rows_pad * 128u + (lane & 3) * 4;
-            uint32_t* sp = scales + (size_t)(2 * kp + (lane >> 4)) * scale_ld;
-            for (int j = 0; j < copies; ++j) {
-                const int prow = __ldg(pr + j);
-                *(uint32_t*)(plane + (size_t)prow * 128u + (((lane >> 2) ^ (prow & 7)) << 4)) = w;
-                if (sc) sp[prow] = sw;
+    for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < n_rows; r += nw)
+        for (int kp = 0; kp < planes; kp += kMxPlanes)
+            round_planes<TYPE>(x, r, n_in, kp, planes, slot_prow + r * copies, copies, o, lane);
+}
+
+// ------------------------------------------- row ids and gather in two launches
+// For up to kRidMaxE experts the tables come from two launches instead of the
+// row-id pass and a gather (35 + 60 us of a 4096-token gate product, 32 + 98 us
+// of the skewed 8192-token one): G CTAs count their tokens' slots by expert;
+// then each CTA sums the counts before its own (the place of its first slot of
+// every expert, the tables' prefixes), ranks its slots in slot order - the same
+// stable counting sort - and rounds its rows straight into their tile rows.
+// The second launch starts while the first runs and fetches its rows into L2.
+constexpr int kMpThreads = 1024;
+constexpr int64_t kMpPrefetch = 512 * 1024;
+
+__device__ __forceinline__ int64_t mp_token(int64_t T, int g, int G) { return T * g / G; }
+
+__global__ void __launch_bounds__(kMpThreads)
+mx4_count_kernel(const int32_t* __restrict__ ids, int64_t T, int k, int E, int32_t* __restrict__ counts, int* hdr) {
+    extern __shared__ int s_cnt[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (__syncthreads_or(threadIdx.x == 0 && read_status(hdr + kHdrStatus) != 0)) return;
+    for (int e = threadIdx.x; e < E; e += kMpThreads) s_cnt[e] = 0;
+    __syncthreads();
+    const int s0 = (int)(mp_token(T, blockIdx.x, gridDim.x) * k), s1 = (int)(mp_token(T, blockIdx.x + 1, gridDim.x) * k);
+    for (int i = s0 + threadIdx.x; i < s1; i += kMpThreads) {
+        const int e = __ldg(ids + i);
+        if ((unsigned)e < (unsigned)E) atomicAdd(&s_cnt[e], 1);  // a count: the order does not matter
+        else set_status(hdr + kHdrStatus, MOE_ERR_BAD_ID);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kMpThreads) counts[(size_t)blockIdx.x * E + e] = s_cnt[e];
+}
+
+struct MxPlaceArgs {
+    const int32_t* ids;
+    const void* x;
+    int n_in;
+    int64_t T;
+    int k, E, per_slot;
+    const int32_t* counts;
+    int32_t *bounds, *ntile_prefix, *pad_start, *ids_dst, *slot_prow;
+    int* hdr;
+    MxRows rows;
+};
+
+// Exclusive prefix over the CTA's 1024 threads (and the total), in thread order.
+__device__ __forceinline__ int cta_prefix(int v, int* warp_sums, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += n;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    const int w = warp_sums[lane];
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    *total = __reduce_add_sync(0xffffffffu, w);
+    __syncthreads();  // warp_sums reusable afterwards
+    return before + incl - v;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs p) {
+    extern __shared__ int s_dyn[];
+    const int E = p.E, G = gridDim.x, g = blockIdx.x, k = p.k;
+    int* s_base = s_dyn;        // [E] sorted position of the CTA's next slot of the expert
+    int* s_delta = s_base + E;  // [E] tile row minus sorted position
+    int* s_row = s_delta + E;   // [32][E] a warp's counts, then its first positions
+    __shared__ int s_sums[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t t0 = mp_token(p.T, g, G), t1 = mp_token(p.T, g + 1, G);
+    const int64_t r0 = p.per_slot ? t0 * k : t0, r1 = p.per_slot ? t1 * k : t1;
+    {  // the CTA's source rows into L2, in pieces of up to 64 KB on 16-byte borders
+        constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
+        const char* a = (const char*)p.x + r0 * p.n_in * esz;
+        // (no more than fits in L2 for all CTAs together)
+        const int64_t all = (r1 - r0) * p.n_in * esz, bytes = all < kMpPrefetch ? all : kMpPrefetch;
+        const int64_t off = (int64_t)tid * 65536;
+        if (off < bytes) ptx::bulk_prefetch_l2(a + off, (uint32_t)(bytes - off < 65536 ? bytes - off : 65536));
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (read_status(p.hdr + kHdrStatus) != 0) return;
+    // counts before this CTA's and in all: 1024 / E threads an expert, each some of the rows
+    const int Ep = (E + 31) & ~31, parts = kMpThreads / Ep;
+    {
+        int before = 0, all = 0;
+        const int e = tid % Ep, part = tid / Ep;
+        if (part < parts && e < E) {
+            int c = part;
+            for (; c + 7 * parts < G; c += 8 * parts) {
+                int v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __ldcg(p.counts + (size_t)(c + i * parts) * E + e);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    all += v[i];
+                    before += c + i * parts < g ? v[i] : 0;
+                }
             }
+            for (; c < G; c += parts) {
+                const int v = __ldcg(p.counts + (size_t)c * E + e);
+                all += v;
+                before += c < g ? v : 0;
+            }
+        }
+        // s_row has room for parts * 2 <= 64 rows of Ep <= 1024 / parts words
+        if (part < parts) {
+            s_row[part * 2 * Ep + e] = before;
+            s_row[(part * 2 + 1) * Ep + e] = all;
+        }
+    }
+    __syncthreads();
+    {
+        int before = 0, all = 0;
+        if (tid < E)
+            for (int i = 0; i < parts; ++i) {
+                before += s_row[i * 2 * Ep + tid];
+                all += s_row[(i * 2 + 1) * Ep + tid];
+            }
+        int S, tiles, padded;
+        const int b = cta_prefix(all, s_sums, &S);
+        const int q = cta_prefix((all + kMxBN - 1) / kMxBN, s_sums, &tiles);
+        const int pad = cta_prefix((all + 7) & ~7, s_sums, &padded);
+        if (tid < E) {
+            s_base[tid] = b + before;
+            s_delta[tid] = pad - b;
+            if (g == 0) {
+                p.bounds[tid] = b;
+                p.ntile_prefix[tid] = q;
+                p.pad_start[tid] = pad;
+            }
+        }
+        if (g == 0 && tid == 0) {
+            p.bounds[E] = S;
+            p.ntile_prefix[E] = tiles;
+            p.pad_start[E] = padded;
+            p.hdr[kHdrTiles] = tiles;
+        }
+    }
+    __syncthreads();
+    // rank the CTA's slots, 1024 at a time: within a warp by ballots, across the
+    // warps by a prefix of their counts
+    const int nb = E > 1 ? 32 - __clz(E - 1) : 1;
+    const int s0 = (int)(t0 * k), s1 = (int)(t1 * k);
+    for (int i0 = s0; i0 < s1; i0 += kMpThreads) {
+        const int nw = min(32, (s1 - i0 + 31) / 32);  // warps with slots
+        for (int i = tid; i < nw * E; i += kMpThreads) s_row[i] = 0;
+        __syncthreads();
+        const int i = i0 + tid;
+        const int e = i < s1 ? __ldg(p.ids + i) : -1;
+        int rank = 0;
+        if (warp < nw) {
+            const unsigned m = match_by_ballots(e, nb);
+            rank = __popc(m & ((1u << lane) - 1u));
+            if (e >= 0 && rank == 0) s_row[warp * E + e] = __popc(m);
+        }
+        __syncthreads();
+        if (tid < E) {
+            int run = s_base[tid];
+            for (int w = 0; w < nw; ++w) {
+                const int c = s_row[w * E + tid];
+                s_row[w * E + tid] = run;
+                run += c;
+            }
+            s_base[tid] = run;
+        }
+        __syncthreads();
+        if (e >= 0) {
+            const int pos = s_row[warp * E + e] + rank;
+            p.ids_dst[pos] = i;
+            p.slot_prow[i] = pos + s_delta[e];
+        }
+        __syncthreads();
+    }
+    // round the CTA's rows, four planes of a row to a warp at a time
+    const int planes = (p.n_in + 255) / 256, chunks = (planes + kMxPlanes - 1) / kMxPlanes, copies = p.per_slot ? 1 : k;
+    const int dr = 32 / chunks, dc = 32 % chunks;
+    int64_t r = r0 + warp / chunks;
+    for (int c = warp % chunks; r < r1; r += dr) {
+        round_planes<TYPE>(p.x, r, p.n_in, c * kMxPlanes, planes, p.slot_prow + r * copies, copies, p.rows, lane);
+        c += dc;
+        if (c >= chunks) {
+            c -= chunks;
+            ++r;
         }
     }
 }
@@ -495,6 +776,31 @@ bool plan_weights(Mx4Params& p, int n_experts) {
     return true;
 }
 
+// A launch that may start before the stream's previous kernel has ended (which
+// lets it, by griddepcontrol.launch_dependents) and waits for it itself.
+template <typename A>
+moe_status launch_dependent(void (*kernel)(A), unsigned grid, int threads, size_t smem, cudaStream_t stream, const A& args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <int TYPE>
+moe_status launch_place(const MxPlaceArgs& a, unsigned grid, size_t smem, cudaStream_t s) {
+    if (cudaFuncSetAttribute(mx4_place_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(34 * kRidMaxE * sizeof(int))) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launch_dependent(mx4_place_kernel<TYPE>, grid, kMpThreads, smem, s, a);
+}
+
 moe_status launch_mx4_gemm(Mx4Params& p, int64_t max_coltiles, cudaStream_t stream) {
     p.wait_limit = kWaitLimitCycles;
     p.stall_cta = -1;
@@ -507,8 +813,7 @@ moe_status launch_mx4_gemm(Mx4Params& p, int64_t max_coltiles, cudaStream_t stre
     const int64_t units = max_coltiles * ((p.L.mt_count + p.tiles_per_unit - 1) / p.tiles_per_unit);
     const int sms = mx_sm_count();
     const unsigned grid = (unsigned)(units < sms ? units : sms);
-    mx4_gemm_kernel<<<grid, kMxThreads, kMxSmem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_dependent(mx4_gemm_kernel, grid, kMxThreads, kMxSmem, stream, p);
 }
 
 }  // namespace
@@ -539,37 +844,60 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     p.W = (const uint8_t*)W_prepared;
     p.L = WLayout(n_out, n_in, MOE_MXFP4);
     if (!plan_weights(p, n_experts)) return MOE_ERR_CUDA;
-    prof_begin(s);
-    int n_rid = 1;
-    moe_status st = launch_row_ids(ids, S, k, n_experts, mode, (int32_t*)(ws + W.src1), (int32_t*)(ws + W.dst),
-                                   (int32_t*)(ws + W.bounds), (int32_t*)(ws + W.active), (int32_t*)(ws + W.tiles),
-                                   (int32_t*)(ws + W.pad), (int32_t*)(ws + W.sprow), kMxBN, hdr,
-                                   n_experts <= kRidMaxE ? (int32_t*)(ws + W.rid) : nullptr, s, &n_rid);
-    if (st) return st;
-    prof_mark(s, "row_ids", n_rid);
     // The rounded rows take the workspace of the 16-bit ones: 128 bytes per 256
     // values and 4 per 128 where those take 128 per 64.  Only up to 64 values do
     // the scales not fit behind the codes; there they take the rows' factors.
-    uint8_t* codes = (uint8_t*)(ws + W.xt);
-    uint32_t* scales = n_in <= kTileK ? (uint32_t*)(ws + W.xs)
-                                      : (uint32_t*)(codes + (size_t)((n_in + 255) / 256) * W.rows_pad * 128u);
-    const int64_t scale_ld = (W.rows_pad + 3) / 4 * 4;  // bulk copies start on 16 bytes
-    const int64_t rows = mode == MOE_BROADCAST ? n_tokens : S, blocks = (rows + 7) / 8;
-    const int64_t cap = (int64_t)mx_sm_count() * 8;
-    mx4_gather_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, s>>>(
-        x, x_type, n_in, (const int32_t*)(ws + W.sprow), mode == MOE_BROADCAST ? k : 1, rows, W.rows_pad, scale_ld,
-        codes, scales, hdr);
-    if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    MxRows o;
+    o.rows_pad = W.rows_pad;
+    o.scale_ld = (W.rows_pad + 3) / 4 * 4;  // bulk copies start on 16 bytes
+    o.codes = (uint8_t*)(ws + W.xt);
+    o.scales = n_in <= kTileK ? (uint32_t*)(ws + W.xs)
+                              : (uint32_t*)(o.codes + (size_t)((n_in + 255) / 256) * W.rows_pad * 128u);
+    const bool broadcast = mode == MOE_BROADCAST;
+    prof_begin(s);
+    moe_status st;
+    if (n_experts <= kRidMaxE) {
+        const unsigned G = (unsigned)(n_tokens < kMxPlaceCtas ? n_tokens : kMxPlaceCtas);
+        int32_t* counts = (int32_t*)(ws + W.rid);
+        mx4_count_kernel<<<G, kMpThreads, (size_t)n_experts * sizeof(int), s>>>(ids, n_tokens, k, n_experts, counts, hdr);
+        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        prof_mark(s, "row_ids");
+        MxPlaceArgs a = {ids, x, n_in, n_tokens, k, n_experts, !broadcast, counts, (int32_t*)(ws + W.bounds),
+                         (int32_t*)(ws + W.tiles), (int32_t*)(ws + W.pad), (int32_t*)(ws + W.dst),
+                         (int32_t*)(ws + W.sprow), hdr, o};
+        const int Ep = (n_experts + 31) & ~31;
+        const size_t rows = 32 * (size_t)n_experts, sums = 2 * (size_t)(kMpThreads / Ep) * Ep;
+        const size_t smem = (2 * (size_t)n_experts + (rows > sums ? rows : sums)) * sizeof(int);
+        st = x_type == MOE_BF16  ? launch_place<MOE_BF16>(a, G, smem, s)
+             : x_type == MOE_F16 ? launch_place<MOE_F16>(a, G, smem, s)
+                                 : launch_place<MOE_F32>(a, G, smem, s);
+    } else {
+        int n_rid = 1;
+        st = launch_row_ids(ids, S, k, n_experts, mode, (int32_t*)(ws + W.src1), (int32_t*)(ws + W.dst),
+                            (int32_t*)(ws + W.bounds), (int32_t*)(ws + W.active), (int32_t*)(ws + W.tiles),
+                            (int32_t*)(ws + W.pad), (int32_t*)(ws + W.sprow), kMxBN, hdr, nullptr, s, &n_rid);
+        if (st) return st;
+        prof_mark(s, "row_ids", n_rid);
+        const int64_t rows = broadcast ? n_tokens : S, blocks = (rows + 7) / 8, cap = (int64_t)mx_sm_count() * 8;
+        const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
+        const int32_t* prow = (const int32_t*)(ws + W.sprow);
+        const int copies = broadcast ? k : 1;
+        if (x_type == MOE_BF16) mx4_gather_kernel<MOE_BF16><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
+        else if (x_type == MOE_F16) mx4_gather_kernel<MOE_F16><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
+        else mx4_gather_kernel<MOE_F32><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
+        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    if (st) return st;
     prof_mark(s, "gather");
     p.tiles_per_unit = 2;
     p.n_groups = n_experts;
     p.bounds = (const int32_t*)(ws + W.bounds);
     p.ntile_prefix = (const int32_t*)(ws + W.tiles);
     p.pad_start = (const int32_t*)(ws + W.pad);
-    p.B = codes;
-    p.BS = scales;
-    p.rows_pad = W.rows_pad;
-    p.scale_ld = scale_ld;
+    p.B = o.codes;
+    p.BS = o.scales;
+    p.rows_pad = o.rows_pad;
+    p.scale_ld = o.scale_ld;
     p.dst_rows = (const int32_t*)(ws + W.dst);
     p.out = dst;
     p.out_ld = n_out;
