@@ -86,6 +86,46 @@ struct Mx4Params {
 // The sub-block row that the 128-byte swizzle puts in place r (and back).
 __device__ __forceinline__ int perm_row(int r) { return r ^ (r >> 3); }
 
+// One thread: the copies of a 128-row tile's stage (codes to `codes`, 4096 bytes
+// a k-step; scales to `scales`, 256 bytes a k-step) and their arrival on `bar`.
+// Of the last, partial tile a k-step is one copy of its 32-row sub-blocks'
+// codes, one of its 16-row sub-block's, and the scales by sub-block (a tensor
+// copy's destination would need 128-byte alignment).
+__device__ __forceinline__ void load_weights(const Mx4Params& p, const WLayout& L, uint8_t* codes, uint8_t* scales, int e,
+                                             int mt, int ks, uint64_t* bar) {
+    if (mt < p.full_tiles) {
+        ptx::mbar_arrive_expect_tx(bar, kMxACodes + kMxAScales);
+        ptx::tma_load_5d(codes, &p.codes, 0, 0, ks * kMxStageKt * 4, mt, e, bar);
+        ptx::tma_load_4d(scales, &p.scales, 0, ks * kMxStageKt * 4, mt, e, bar);
+        return;
+    }
+    const int kts = min(kMxStageKt, L.kt_count - ks * kMxStageKt);
+    ptx::mbar_arrive_expect_tx(bar, (uint32_t)(kts * L.rows(mt) * kRowBytesMx));
+    for (int j = 0; j < kts; ++j, codes += kMxCodes, scales += 256) {
+        const int kt = ks * kMxStageKt + j;
+        const uint8_t* src = p.W + L.block(e, mt, kt);
+        if (p.tail_subs) ptx::tma_load_5d(codes, &p.t_codes, 0, 0, 0, kt, e, bar);
+        if (p.tail_r) ptx::tma_load_5d(codes + p.tail_subs * 1024, &p.r_codes, 0, 0, 0, kt, e, bar);
+        for (int sb = 0; sb < p.tail_subs; ++sb)
+            ptx::bulk_g2s(scales + sb * 64, src + sb * (kSubRows * kRowBytesMx) + kSubRows * 32, kSubRows * 2, bar);
+        if (p.tail_r)
+            ptx::bulk_g2s(scales + p.tail_subs * 64, src + p.tail_subs * (kSubRows * kRowBytesMx) + 16 * 32, 16 * 2, bar);
+    }
+}
+
+// The scales of a 128-row tile's stage at `as` as this lane's eight words of
+// tensor memory (two 128-value halves x four rows 32 apart).
+__device__ __forceinline__ void weight_scales(uint32_t as, int lane, uint32_t* v) {
+    as += perm_row(lane) * 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int sb = 0; sb < 4; ++sb) {
+            const uint32_t a = as + h * 512 + sb * 64;
+            v[h * 4 + sb] = ptx::lds16(a) | ptx::lds16(a + 256) << 16;
+        }
+}
+
 struct MxTile {
     int e, mu, p0, n, p0pad;
 };
@@ -168,20 +208,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         return r;
     };
 
-    // One k-step of the last, partial tile: its 32-row sub-blocks' codes in one
-    // tensor copy, its 16-row sub-block's in another, the scales by sub-block
-    // (a tensor copy's destination would need 128-byte alignment).
-    auto load_tail = [&](uint8_t* codes, uint8_t* scales, int e, int kt, uint64_t* bar) {
-        const uint8_t* src = p.W + L.block(e, MT - 1, kt);
-        if (p.tail_subs) ptx::tma_load_5d(codes, &p.t_codes, 0, 0, 0, kt, e, bar);
-        if (p.tail_r) ptx::tma_load_5d(codes + p.tail_subs * 1024, &p.r_codes, 0, 0, 0, kt, e, bar);
-        for (int sb = 0; sb < p.tail_subs; ++sb)
-            ptx::bulk_g2s(scales + sb * 64, src + sb * (kSubRows * kRowBytesMx) + kSubRows * 32, kSubRows * 2, bar);
-        if (p.tail_r)
-            ptx::bulk_g2s(scales + p.tail_subs * 64, src + p.tail_subs * (kSubRows * kRowBytesMx) + 16 * 32, 16 * 2,
-                          bar);
-    };
-
     if (warp == 0 || warp == 2 || warp == 3) {
         // ------------------------------------------------------------ copies
         // Warps 0 and 2: the codes and scales of the unit's first and second
@@ -219,19 +245,9 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                         par = (par & ~(1u << s)) | (ph << s);
                     }
                 } else if (issue) {
-                    uint8_t* ac = st + i * kMxACodes;
-                    uint8_t* as = st + kMxOffAS + i * kMxAScales;
-                    if (i < TPU && mt < p.full_tiles) {
-                        ptx::mbar_arrive_expect_tx(&full[s], kMxACodes + kMxAScales);
-                        ptx::tma_load_5d(ac, &p.codes, 0, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
-                        ptx::tma_load_4d(as, &p.scales, 0, ks * kMxStageKt * 4, mt, u.e, &full[s]);
-                    } else if (i < TPU && mt < MT) {
-                        ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)(kts * L.rows(mt) * kRowBytesMx));
-                        for (int j = 0; j < kts; ++j)
-                            load_tail(ac + j * kMxCodes, as + j * 256, u.e, ks * kMxStageKt + j, &full[s]);
-                    } else {
-                        ptx::mbar_arrive(&full[s]);
-                    }
+                    if (i < TPU && mt < MT)
+                        load_weights(p, L, st + i * kMxACodes, st + kMxOffAS + i * kMxAScales, u.e, mt, ks, &full[s]);
+                    else ptx::mbar_arrive(&full[s]);
                 }
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
@@ -304,18 +320,11 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
             for (int ks = 0; ks < KS; ++ks) {
                 ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
-                const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS) + perm_row(lane) * 2;
+                const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS);
                 const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 4;
                 uint32_t v[32];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int sb = 0; sb < 4; ++sb) {
-                            const uint32_t a = as + i * kMxAScales + h * 512 + sb * 64;
-                            v[i * 8 + h * 4 + sb] = ptx::lds16(a) | ptx::lds16(a + 256) << 16;
-                        }
+                weight_scales(as, lane, v);
+                weight_scales(as + kMxAScales, lane, v + 8);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -701,6 +710,318 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
     }
 }
 
+// ------------------------------------------------- few slots: one launch
+// Up to kMdMaxSlots slots the call is bound by launches and latency, and then
+// by the touched experts' bytes, so one launch does it all: every CTA finds the
+// experts and their slots from the ids itself (up to kMdN slots of an expert
+// are a group), takes a contiguous range of (group, 128-row tile) items, rounds
+// its group's rows into shared memory - all of K, they are few - while the
+// weights already stream into a ring, and runs the MMAs 16 columns wide.
+constexpr int kMdThreads = 384;
+constexpr int kMdWorkers = 256;     // warps 4-11
+constexpr int kMdMaxSlots = 256;
+constexpr int kMdN = 16;            // columns of an accumulator
+constexpr int kMdMaxPlanes = 48;    // K up to 12288
+constexpr int kMdMaxStages = 10;
+constexpr uint32_t kMdStage = kMxACodes + kMxAScales;
+constexpr uint32_t kMdPlane = kMdN * 128, kMdPlaneScales = 2 * kMdN * 4;
+constexpr uint32_t kMdSmem = 211 * 1024;
+// tensor memory: two accumulators, the stages' A scales (8 columns each), the B
+// scales of all of K (4 columns per 128 values, of which 16 rows take the first)
+constexpr uint32_t kMdColA = 2 * kMdN, kMdColB = kMdColA + 8 * kMdMaxStages;
+static_assert(kMdColA % 4 == 0 && kMdColB % 4 == 0 && kMdColB + 8 * kMdMaxPlanes <= 512, "tensor memory");
+constexpr int kMdBarRed = 1;  // named barrier of the workers
+
+struct MxDecodeArgs {
+    Mx4Params w;  // weights, output, status
+    const int32_t* ids;
+    const void* x;
+    int n_in, S, k, E, per_slot, stages;
+};
+
+template <int TYPE>
+__global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_constant__ MxDecodeArgs a) {
+    extern __shared__ uint8_t smem_dyn[];
+    __shared__ __align__(16) int s_ids[kMdMaxSlots];
+    __shared__ __align__(16) int s_pass[kMdMaxSlots];  // of an expert's first slot: its groups; 0 elsewhere
+    __shared__ int s_base[kMdMaxSlots];                // of an expert's first slot: its first group
+    __shared__ short s_first[kMdMaxSlots], s_before[kMdMaxSlots];  // the expert's first slot, its slots before this one
+    __shared__ int s_expert[kMdMaxSlots];              // of a group
+    __shared__ short s_count[kMdMaxSlots], s_slots[kMdMaxSlots][kMdN];
+    __shared__ uint64_t s_bar[3 * kMdMaxStages + 6];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_groups, s_stop;
+
+    const Mx4Params& p = a.w;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WLayout L = p.L;
+    const int MT = L.mt_count, KT = L.kt_count, KS = (KT + kMxStageKt - 1) / kMxStageKt, NS = a.stages, S = a.S;
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_dyn + 1023) & ~(uintptr_t)1023);
+    uint8_t* s_b = smem;                                        // [plane][16][128]
+    uint8_t* ring = smem + (size_t)KS * kMdPlane;               // codes of the stages
+    uint8_t* ring_s = ring + (size_t)NS * kMxACodes;            // scales of the stages
+    uint32_t* s_bs = (uint32_t*)(ring_s + (size_t)NS * kMxAScales);  // [K / 128][16]
+    uint64_t* full = s_bar;
+    uint64_t* sf_full = full + kMdMaxStages;
+    uint64_t* empty = sf_full + kMdMaxStages;
+    uint64_t* b_full = empty + kMdMaxStages;  // the group's rows and their scales are in place
+    uint64_t* acc_full = b_full + 1;          // [2]
+    uint64_t* acc_empty = acc_full + 2;       // [2]
+    uint64_t* drained = acc_empty + 2;
+    volatile int* abort_flag = &s_abort;
+    int* status = p.hdr + kHdrStatus;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&sf_full[i], 4);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        ptx::mbar_init(b_full, 4);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&acc_full[i], 1);
+            ptx::mbar_init(&acc_empty[i], 4);
+        }
+        ptx::mbar_init(drained, 1);
+        s_abort = 0;
+        s_groups = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&s_tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    // (starts before the stream's previous kernel has ended, and lets the next one do so)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tid == 0) s_stop = read_status(status) != 0;
+    int bad = 0;
+    const int S4 = (S + 3) & ~3;
+    for (int i = tid; i < S4; i += kMdThreads) {
+        const int e = i < S ? __ldg(a.ids + i) : -1;
+        bad |= i < S && (unsigned)e >= (unsigned)a.E;
+        s_ids[i] = e;
+        s_pass[i] = 0;
+    }
+    if (bad) set_status(status, MOE_ERR_BAD_ID);
+    const bool stop = __syncthreads_or(bad) || s_stop;
+    // groups: every slot against all others, four ids a load
+    if (tid < S && !stop) {
+        const int e = s_ids[tid];
+        int before = 0, all = 0, first = tid;
+        for (int j = 0; j < S4; j += 4) {
+            const int4 v = *(const int4*)(s_ids + j);
+            const int m[4] = {v.x == e, v.y == e, v.z == e, v.w == e};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                all += m[q];
+                if (m[q] && j + q < tid) {
+                    ++before;
+                    first = min(first, j + q);
+                }
+            }
+        }
+        s_first[tid] = (short)first;
+        s_before[tid] = (short)before;
+        if (before == 0) s_pass[tid] = (all + kMdN - 1) / kMdN;
+        s_base[tid] = all;
+    }
+    __syncthreads();
+    if (tid < S && !stop && s_pass[tid] > 0) {
+        const int all = s_base[tid], n = s_pass[tid];
+        int base = 0;
+        for (int j = 0; j < tid; j += 4) {
+            const int4 v = *(const int4*)(s_pass + j);
+            base += v.x + (j + 1 < tid ? v.y : 0) + (j + 2 < tid ? v.z : 0) + (j + 3 < tid ? v.w : 0);
+        }
+        s_base[tid] = base;
+        for (int g = 0; g < n; ++g) {
+            s_expert[base + g] = s_ids[tid];
+            s_count[base + g] = (short)min(kMdN, all - g * kMdN);
+        }
+        atomicAdd(&s_groups, n);
+    }
+    __syncthreads();
+    if (tid < S && !stop) {
+        const int before = s_before[tid];
+        s_slots[s_base[s_first[tid]] + before / kMdN][before % kMdN] = (short)tid;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int items = s_groups * MT;
+    const int it0 = (int)((int64_t)items * blockIdx.x / gridDim.x), it1 = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ weights
+        const uint32_t issue = ptx::elect_one();
+        int s = 0, q = 0;
+        uint32_t ph = 0, used = 0, par = 0;
+        bool ok = true;
+        for (int it = it0; it < it1 && ok; ++it) {
+            const int e = s_expert[it / MT], mt = it % MT;
+            for (int ks = 0; ks < KS; ++ks, ++q) {
+                ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                if (!((int)blockIdx.x == p.stall_cta && q == p.stall_stage)) {
+                    if (issue)
+                        load_weights(p, L, ring + (size_t)s * kMxACodes, ring_s + (size_t)s * kMxAScales, e, mt, ks,
+                                     &full[s]);
+                    used |= 1u << s;
+                    par = (par & ~(1u << s)) | (ph << s);
+                }
+                __syncwarp();
+                if (++s == NS) { s = 0; ph ^= 1; }
+            }
+        }
+        // let every copy issued land before the CTA can exit (bounded)
+        volatile int never = 0;
+        for (int j = 0; j < NS; ++j)
+            if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, p.wait_limit);
+    } else if (warp == 1) {
+        // --------------------------------------------------------------- MMAs
+        const uint32_t issue = ptx::elect_one(), ring_a = ptx::smem_u32(ring), b_a = ptx::smem_u32(s_b);
+        const uint32_t id0 = ptx::idesc_mxf4(kMdN, 0), id1 = ptx::idesc_mxf4(kMdN, 1);
+        int s = 0;
+        uint32_t ph = 0, n = 0;
+        bool ok = true;
+        for (int it = it0; it < it1 && ok; ++it, ++n) {
+            const uint32_t buf = n & 1;
+            ok = warp_wait(b_full, n & 1, abort_flag, status, p.wait_limit) &&
+                 warp_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag, status, p.wait_limit);
+            if (!ok) break;
+            for (int ks = 0; ks < KS; ++ks) {
+                ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
+                     warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t ad = ptx::desc_k_sw32(ring_a + (uint32_t)s * kMxACodes);
+                const uint64_t bd = ptx::desc_k_sw128(b_a + (uint32_t)ks * kMdPlane);
+                const uint32_t sfa = tmem + kMdColA + (uint32_t)s * 8u, sfb = tmem + kMdColB + (uint32_t)ks * 8u;
+                const int kts = KT - ks * kMxStageKt;
+#pragma unroll
+                for (int j = 0; j < kMxStageKt; ++j)
+                    if (j < kts)
+                        ptx::mma_mxf4_ss(tmem + buf * kMdN, ad + (j * kMxCodes >> 4), bd + j * 2, j & 1 ? id1 : id0,
+                                         sfa + (j >> 1) * 4, sfb + (j >> 1) * 4, (ks | j) != 0, issue);
+                if (issue) ptx::mma_commit(&empty[s]);
+                __syncwarp();
+                if (++s == NS) { s = 0; ph ^= 1; }
+            }
+            if (!ok) break;
+            if (issue) ptx::mma_commit(&acc_full[buf]);
+            __syncwarp();
+        }
+        if (issue) {
+            ptx::mma_commit(drained);
+            volatile int never = 0;
+            wait_bar(drained, 0, &never, status, p.wait_limit);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ workers
+        // All eight warps round a new group's rows; warps 4-7 then move the scales
+        // and drain the accumulator.  Every worker passes the same barriers: one
+        // that has given up says so at the next, and all leave there.
+        const int w = warp - 4, wq = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
+        constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
+        int s = 0, group = -1;
+        uint32_t ph = 0, n = 0;
+        bool ok = true;
+        for (int it = it0; it < it1; ++it, ++n) {
+            const int g = it / MT, mt = it % MT, rows = s_count[g];
+            ok = ptx::bar_red_and(kMdBarRed, kMdWorkers, ok);
+            if (!ok) break;
+            if (g != group) {  // (the MMAs of the last group have completed: acc_full below)
+                group = g;
+                const int units = rows * KS;
+                for (int u0 = w; u0 < units; u0 += 8 * kMxPlanes) {
+                    MxEight<TYPE> v[kMxPlanes];
+#pragma unroll
+                    for (int i = 0; i < kMxPlanes; ++i) {
+                        const int u = u0 + 8 * i, r = u / KS, col = (u - r * KS) * 256 + lane * 8;
+                        if (u < units && col < a.n_in) {
+                            const int slot = s_slots[g][r];
+                            const int64_t row = a.per_slot ? slot : slot / a.k;
+                            v[i].load((const char*)a.x + (row * a.n_in + col) * esz);
+                        } else {
+                            v[i].zero();
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kMxPlanes; ++i) {
+                        const int u = u0 + 8 * i, r = u / KS, kp = u - r * KS;
+                        if (u >= units) break;
+                        uint32_t m = v[i].amax_bits();
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                        const uint32_t X = mx_scale_byte(m);
+                        const uint32_t c = X == 255u ? 0u : v[i].codes(mx_inv_scale(X));
+                        uint32_t sw = X << (8 * ((lane >> 2) & 3));
+                        sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
+                        sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
+                        *(uint32_t*)(s_b + (size_t)kp * kMdPlane + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                     (lane & 3) * 4) = c;
+                        if ((lane & 15) == 0) s_bs[(2 * kp + (lane >> 4)) * kMdN + r] = sw;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::bar_red_and(kMdBarRed, kMdWorkers, true);
+                if (w < 4) {
+                    ptx::tc_fence_after();
+                    for (int c = 0; c < 2 * KS; ++c)
+                        ptx::tmem_st_32x32b_x1(lanes + kMdColB + c * 4, s_bs[c * kMdN + (lane & 15)]);
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                }
+            }
+            const uint32_t buf = n & 1;
+            if (w < 4) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(b_full);
+                for (int ks = 0; ks < KS && ok; ++ks) {
+                    ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
+                    if (!ok) break;
+                    uint32_t v[8];
+                    weight_scales(ptx::smem_u32(ring_s + (size_t)s * kMxAScales), lane, v);
+                    ptx::tc_fence_after();
+                    ptx::tmem_st_32x32b_x8(lanes + kMdColA + (uint32_t)s * 8u, v);
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sf_full[s]);
+                    if (++s == NS) { s = 0; ph ^= 1; }
+                }
+            }
+            ok = ok && warp_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, status, p.wait_limit);
+            if (ok && w < 4) {
+                ptx::tc_fence_after();
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(lanes + buf * kMdN, v);
+                ptx::tmem_ld_wait();
+                const int m = mt * kTileM + 32 * wq + perm_row(lane);
+                if (m < L.n_out) {
+#pragma unroll
+                    for (int j = 0; j < kMdN; ++j)
+                        if (j < rows) p.out[(int64_t)s_slots[g][j] * p.out_ld + m] = __uint_as_float(v[j]);
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
 // ------------------------------------------------------------------- host
 int mx_sm_count() {
     static std::atomic<int> cached[64];
@@ -801,12 +1122,17 @@ moe_status launch_place(const MxPlaceArgs& a, unsigned grid, size_t smem, cudaSt
     return launch_dependent(mx4_place_kernel<TYPE>, grid, kMpThreads, smem, s, a);
 }
 
-moe_status launch_mx4_gemm(Mx4Params& p, int64_t max_coltiles, cudaStream_t stream) {
-    p.wait_limit = kWaitLimitCycles;
-    p.stall_cta = -1;
-    p.stall_stage = 0;
-    long long limit = 0;
-    if (testing_stall_state(&p.stall_cta, &p.stall_stage, &limit)) p.wait_limit = limit;
+template <int TYPE>
+moe_status launch_decode(const MxDecodeArgs& a, cudaStream_t s) {
+    if (cudaFuncSetAttribute(mx4_decode_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMdSmem) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    const int64_t items = (int64_t)a.S * a.w.L.mt_count;  // at most: a group has a slot
+    const int sms = mx_sm_count();
+    return launch_dependent(mx4_decode_kernel<TYPE>, (unsigned)(items < sms ? items : sms), kMdThreads, kMdSmem, s, a);
+}
+
+moe_status launch_mx4_gemm(const Mx4Params& p, int64_t max_coltiles, cudaStream_t stream) {
     if (cudaFuncSetAttribute(mx4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMxSmem) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
@@ -844,6 +1170,33 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     p.W = (const uint8_t*)W_prepared;
     p.L = WLayout(n_out, n_in, MOE_MXFP4);
     if (!plan_weights(p, n_experts)) return MOE_ERR_CUDA;
+    p.out = dst;
+    p.out_ld = n_out;
+    p.hdr = hdr;
+    p.wait_limit = kWaitLimitCycles;
+    p.stall_cta = -1;
+    long long limit = 0;
+    if (testing_stall_state(&p.stall_cta, &p.stall_stage, &limit)) p.wait_limit = limit;
+    const int planes = (n_in + 255) / 256;
+    if (S <= kMdMaxSlots && planes <= kMdMaxPlanes) {
+        MxDecodeArgs a = {};
+        a.w = p;
+        a.ids = ids;
+        a.x = x;
+        a.n_in = n_in;
+        a.S = (int)S;
+        a.k = k;
+        a.E = n_experts;
+        a.per_slot = mode == MOE_PER_SLOT;
+        const int room = (int)((kMdSmem - 1024 - planes * (kMdPlane + kMdPlaneScales)) / kMdStage);
+        a.stages = room < kMdMaxStages ? room : kMdMaxStages;
+        prof_begin(s);
+        const moe_status st = x_type == MOE_BF16  ? launch_decode<MOE_BF16>(a, s)
+                              : x_type == MOE_F16 ? launch_decode<MOE_F16>(a, s)
+                                                  : launch_decode<MOE_F32>(a, s);
+        prof_mark(s, "decode");
+        return st;
+    }
     // The rounded rows take the workspace of the 16-bit ones: 128 bytes per 256
     // values and 4 per 128 where those take 128 per 64.  Only up to 64 values do
     // the scales not fit behind the codes; there they take the rows' factors.
@@ -852,7 +1205,7 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     o.scale_ld = (W.rows_pad + 3) / 4 * 4;  // bulk copies start on 16 bytes
     o.codes = (uint8_t*)(ws + W.xt);
     o.scales = n_in <= kTileK ? (uint32_t*)(ws + W.xs)
-                              : (uint32_t*)(o.codes + (size_t)((n_in + 255) / 256) * W.rows_pad * 128u);
+                              : (uint32_t*)(o.codes + (size_t)planes * W.rows_pad * 128u);
     const bool broadcast = mode == MOE_BROADCAST;
     prof_begin(s);
     moe_status st;
@@ -899,9 +1252,6 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     p.rows_pad = o.rows_pad;
     p.scale_ld = o.scale_ld;
     p.dst_rows = (const int32_t*)(ws + W.dst);
-    p.out = dst;
-    p.out_ld = n_out;
-    p.hdr = hdr;
     st = launch_mx4_gemm(p, (S + kMxBN - 1) / kMxBN + (S < n_experts ? S : n_experts), s);
     prof_mark(s, "gemm");
     return st;
