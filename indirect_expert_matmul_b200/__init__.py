@@ -9,6 +9,7 @@ fallback, and importing fails loudly if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -305,6 +306,16 @@ def mul_mat_id(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None, out
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _prepared_bytes(w, n_experts, n_out, n_in):
+    return _L().moe_weights_prepared_size_w(w, n_experts, n_out, n_in)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(n_tokens, k, n_experts, n_in, xt):
+    return _L().moe_workspace_size(n_tokens, k, n_experts, n_in, 0, 0, xt)
+
+
 def mul_mat_id_mx4(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None, out=None):
     """dst float32 [T][k][n_out] = W[ids[t][s]] . Q(x[t or (t, s)]), both operands
     in MXFP4 (moe_mul_mat_id_mx4): W prepared with wtype "mxfp4", x rounded to
@@ -324,10 +335,10 @@ def mul_mat_id_mx4(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None,
     if out is None:
         out = torch.empty((T, k, n_out), dtype=torch.float32, device=dev)
     _call("moe_mul_mat_id_mx4", dev, L.moe_mul_mat_id_mx4,
-          _at(W, "W", torch.uint8, L.moe_weights_prepared_size_w(MXFP4, n_experts, n_out, n_in), dev),
+          _at(W, "W", torch.uint8, _prepared_bytes(MXFP4, n_experts, n_out, n_in), dev),
           n_experts, n_out, n_in, _at(x, "x", x.dtype, (T if m == BROADCAST else T * k) * n_in, dev), xt,
           ids.data_ptr(), T, k, m, _at(out, "out", torch.float32, T * k * n_out, dev),
-          _at(ws, "ws", torch.uint8, L.moe_workspace_size(T, k, n_experts, n_in, 0, 0, xt), dev))
+          _at(ws, "ws", torch.uint8, _workspace_bytes(T, k, n_experts, n_in, xt), dev))
     if own_ws:
         _chk(get_status(ws), "moe_mul_mat_id_mx4 (device status)")
     return out

@@ -126,6 +126,10 @@ __device__ __forceinline__ void weight_scales(uint32_t as, int lane, uint32_t* v
         }
 }
 
+// A value that is the same in all lanes, so that the compiler knows it.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 struct MxTile {
     int e, mu, p0, n, p0pad;
 };
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
     // (all threads by one thread's reading: another CTA may set the status meanwhile)
     if (tid == 0) s_total = read_status(status) != 0 ? 0 : p.hdr[kHdrTiles] * MU;
     __syncthreads();
-    const int total = s_total;
+    const int total = uniform(s_total);
     if (in_smem && total > 0)
         for (int i = tid; i <= p.n_groups; i += kMxThreads) {
             s_prefix[i] = p.ntile_prefix[i];
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = uniform(s_tmem);
 
     auto unit = [&](int t) {
         MxTile r;
@@ -274,8 +278,8 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
             if (!ok) break;
             use += 1;
             for (int ks = 0; ks < KS; ++ks) {
-                ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
-                     warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+                // (the scale warps arrive after they have seen the stage's copies land)
+                ok = warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t st = smem_a + (uint32_t)s * kMxStagePitch;
@@ -717,18 +721,26 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
 // are a group), takes a contiguous range of (group, 128-row tile) items, rounds
 // its group's rows into shared memory - all of K, they are few - while the
 // weights already stream into a ring, and runs the MMAs 16 columns wide.
+// Roles: warp 0 copies weights, warp 1 issues the MMAs, warps 4-7 move the
+// weights' scales as the stages land, so that by the time warps 2, 3 and 8-11
+// have rounded the rows the ring is ready for the MMAs; warps 8-11 drain the
+// accumulator.
 constexpr int kMdThreads = 384;
-constexpr int kMdWorkers = 256;     // warps 4-11
+constexpr int kMdRounders = 6;      // warps 2, 3, 8-11
 constexpr int kMdMaxSlots = 256;
 constexpr int kMdN = 16;            // columns of an accumulator
-constexpr int kMdMaxPlanes = 48;    // K up to 12288
+constexpr int kMdMaxPlanes = 36;    // K up to 9216
 constexpr int kMdMaxStages = 10;
 constexpr uint32_t kMdStage = kMxACodes + kMxAScales;
 constexpr uint32_t kMdPlane = kMdN * 128, kMdPlaneScales = 2 * kMdN * 4;
 constexpr uint32_t kMdSmem = 211 * 1024;
-// tensor memory: two accumulators, the stages' A scales (8 columns each), the B
-// scales of all of K (4 columns per 128 values, of which 16 rows take the first)
-constexpr uint32_t kMdColA = 2 * kMdN, kMdColB = kMdColA + 8 * kMdMaxStages;
+// Tensor memory: two times four accumulators (MMAs into one accumulator wait for
+// one another, ~170 cycles each however narrow; k-step j of a stage goes to
+// accumulator j and the drain adds the four), the stages' A scales (8 columns
+// each), the B scales of all of K (4 columns per 128 values, 16 rows take the
+// first).
+constexpr uint32_t kMdAcc = kMxStageKt * kMdN;
+constexpr uint32_t kMdColA = 2 * kMdAcc, kMdColB = kMdColA + 8 * kMdMaxStages;
 static_assert(kMdColA % 4 == 0 && kMdColB % 4 == 0 && kMdColB + 8 * kMdMaxPlanes <= 512, "tensor memory");
 constexpr int kMdBarRed = 1;  // named barrier of the workers
 
@@ -745,9 +757,9 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
     __shared__ __align__(16) int s_ids[kMdMaxSlots];
     __shared__ __align__(16) int s_pass[kMdMaxSlots];  // of an expert's first slot: its groups; 0 elsewhere
     __shared__ int s_base[kMdMaxSlots];                // of an expert's first slot: its first group
-    __shared__ short s_first[kMdMaxSlots], s_before[kMdMaxSlots];  // the expert's first slot, its slots before this one
     __shared__ int s_expert[kMdMaxSlots];              // of a group
-    __shared__ short s_count[kMdMaxSlots], s_slots[kMdMaxSlots][kMdN];
+    __shared__ short s_count[kMdMaxSlots];
+    __shared__ __align__(4) short s_slots[kMdMaxSlots][kMdN];
     __shared__ uint64_t s_bar[3 * kMdMaxStages + 6];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_groups, s_stop;
@@ -771,20 +783,21 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
     volatile int* abort_flag = &s_abort;
     int* status = p.hdr + kHdrStatus;
 
-    if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            ptx::mbar_init(&full[i], 1);
-            ptx::mbar_init(&sf_full[i], 4);
-            ptx::mbar_init(&empty[i], 1);
+    // (warp 0 goes straight for the ids)
+    if (warp == 2) {
+        if (lane < NS) {
+            ptx::mbar_init(&full[lane], 1);
+            ptx::mbar_init(&sf_full[lane], 4);
+            ptx::mbar_init(&empty[lane], 1);
         }
-        ptx::mbar_init(b_full, 4);
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&acc_full[i], 1);
-            ptx::mbar_init(&acc_empty[i], 4);
+        if (lane >= 16 && lane < 18) {
+            ptx::mbar_init(&acc_full[lane - 16], 1);
+            ptx::mbar_init(&acc_empty[lane - 16], 4);
         }
-        ptx::mbar_init(drained, 1);
-        s_abort = 0;
-        s_groups = 0;
+        if (lane == 18) ptx::mbar_init(b_full, 4);
+        if (lane == 19) ptx::mbar_init(drained, 1);
+        if (lane == 20) s_abort = 0;
+        if (lane == 21 && S > 32) s_groups = 0;
         ptx::fence_mbar_init();
     }
     if (warp == 1) {
@@ -794,63 +807,91 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
     // (starts before the stream's previous kernel has ended, and lets the next one do so)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid == 0) s_stop = read_status(status) != 0;
-    int bad = 0;
-    const int S4 = (S + 3) & ~3;
-    for (int i = tid; i < S4; i += kMdThreads) {
-        const int e = i < S ? __ldg(a.ids + i) : -1;
-        bad |= i < S && (unsigned)e >= (unsigned)a.E;
-        s_ids[i] = e;
-        s_pass[i] = 0;
+    if (warp == 3 && lane < 4) {
+        // this CTA's share of x into L2, while the groups are found
+        const int64_t all = (int64_t)(a.per_slot ? S : S / a.k) * a.n_in * (TYPE == MOE_F32 ? 4 : 2);
+        const int64_t share = (all / gridDim.x + 127) / 128 * 128, x0 = share * blockIdx.x + lane * 65536;
+        const int64_t x1 = min(all, share * (blockIdx.x + 1)), n = min(x1 - x0, (int64_t)65536);
+        if (n > 0) ptx::bulk_prefetch_l2((const char*)a.x + x0, (uint32_t)n);
     }
-    if (bad) set_status(status, MOE_ERR_BAD_ID);
-    const bool stop = __syncthreads_or(bad) || s_stop;
-    // groups: every slot against all others, four ids a load
-    if (tid < S && !stop) {
-        const int e = s_ids[tid];
-        int before = 0, all = 0, first = tid;
-        for (int j = 0; j < S4; j += 4) {
-            const int4 v = *(const int4*)(s_ids + j);
-            const int m[4] = {v.x == e, v.y == e, v.z == e, v.w == e};
+    const int S4 = (S + 3) & ~3;
+    if (S <= 32) {
+        // one warp finds the groups: equal ids by a warp match
+        if (warp == 0) {
+            const bool stop = read_status(status) != 0;
+            const int e = lane < S ? __ldg(a.ids + lane) : -1;
+            const bool bad = lane < S && (unsigned)e >= (unsigned)a.E;
+            if (bad) set_status(status, MOE_ERR_BAD_ID);
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const int before = __popc(same & ((1u << lane) - 1u)), all = __popc(same), first = __ffs(same) - 1;
+            const int n = lane < S && before == 0 ? (all + kMdN - 1) / kMdN : 0;
+            int base = n;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                all += m[q];
-                if (m[q] && j + q < tid) {
-                    ++before;
-                    first = min(first, j + q);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, base, o);
+                if (lane >= o) base += v;
+            }
+            const bool none = __any_sync(0xffffffffu, bad || stop);
+            if (lane == 31) s_groups = none ? 0 : base;
+            base -= n;
+            for (int g = 0; g < n; ++g) {
+                s_expert[base + g] = e;
+                s_count[base + g] = (short)min(kMdN, all - g * kMdN);
+            }
+            base = __shfl_sync(0xffffffffu, base, first);
+            if (lane < S) s_slots[base + before / kMdN][before % kMdN] = (short)lane;
+        }
+    } else {
+        // every slot against all others, four ids a load
+        if (tid == 0) s_stop = read_status(status) != 0;
+        int bad = 0;
+        if (tid < S4) {
+            const int e = tid < S ? __ldg(a.ids + tid) : -1;
+            bad = tid < S && (unsigned)e >= (unsigned)a.E;
+            s_ids[tid] = e;
+            s_pass[tid] = 0;
+        }
+        if (bad) set_status(status, MOE_ERR_BAD_ID);
+        const bool mine = !__syncthreads_or(bad) && !s_stop && tid < S;
+        int before = 0, all = 0, first = tid, n = 0;
+        if (mine) {
+            const int e = s_ids[tid];
+            for (int j = 0; j < S4; j += 4) {
+                const int4 v = *(const int4*)(s_ids + j);
+                const int m[4] = {v.x == e, v.y == e, v.z == e, v.w == e};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    all += m[q];
+                    if (m[q] && j + q < tid) {
+                        ++before;
+                        first = min(first, j + q);
+                    }
                 }
             }
+            if (before == 0) s_pass[tid] = n = (all + kMdN - 1) / kMdN;
         }
-        s_first[tid] = (short)first;
-        s_before[tid] = (short)before;
-        if (before == 0) s_pass[tid] = (all + kMdN - 1) / kMdN;
-        s_base[tid] = all;
-    }
-    __syncthreads();
-    if (tid < S && !stop && s_pass[tid] > 0) {
-        const int all = s_base[tid], n = s_pass[tid];
-        int base = 0;
-        for (int j = 0; j < tid; j += 4) {
-            const int4 v = *(const int4*)(s_pass + j);
-            base += v.x + (j + 1 < tid ? v.y : 0) + (j + 2 < tid ? v.z : 0) + (j + 3 < tid ? v.w : 0);
+        __syncthreads();
+        if (n > 0) {
+            int base = 0;
+            for (int j = 0; j < tid; j += 4) {
+                const int4 v = *(const int4*)(s_pass + j);
+                base += v.x + (j + 1 < tid ? v.y : 0) + (j + 2 < tid ? v.z : 0) + (j + 3 < tid ? v.w : 0);
+            }
+            s_base[tid] = base;
+            for (int g = 0; g < n; ++g) {
+                s_expert[base + g] = s_ids[tid];
+                s_count[base + g] = (short)min(kMdN, all - g * kMdN);
+            }
+            atomicAdd(&s_groups, n);  // a count: the order does not matter
         }
-        s_base[tid] = base;
-        for (int g = 0; g < n; ++g) {
-            s_expert[base + g] = s_ids[tid];
-            s_count[base + g] = (short)min(kMdN, all - g * kMdN);
-        }
-        atomicAdd(&s_groups, n);
-    }
-    __syncthreads();
-    if (tid < S && !stop) {
-        const int before = s_before[tid];
-        s_slots[s_base[s_first[tid]] + before / kMdN][before % kMdN] = (short)tid;
+        __syncthreads();
+        if (mine) s_slots[s_base[first] + before / kMdN][before % kMdN] = (short)tid;
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    const int items = s_groups * MT;
+    const uint32_t tmem = uniform(s_tmem);
+    const int items = uniform(s_groups) * MT;
     const int it0 = (int)((int64_t)items * blockIdx.x / gridDim.x), it1 = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
 
     if (warp == 0) {
@@ -892,8 +933,8 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                  warp_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag, status, p.wait_limit);
             if (!ok) break;
             for (int ks = 0; ks < KS; ++ks) {
-                ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
-                     warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+                // (the scale warps arrive after they have seen the stage's copies land)
+                ok = warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint64_t ad = ptx::desc_k_sw32(ring_a + (uint32_t)s * kMxACodes);
@@ -903,8 +944,8 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
 #pragma unroll
                 for (int j = 0; j < kMxStageKt; ++j)
                     if (j < kts)
-                        ptx::mma_mxf4_ss(tmem + buf * kMdN, ad + (j * kMxCodes >> 4), bd + j * 2, j & 1 ? id1 : id0,
-                                         sfa + (j >> 1) * 4, sfb + (j >> 1) * 4, (ks | j) != 0, issue);
+                        ptx::mma_mxf4_ss(tmem + buf * kMdAcc + j * kMdN, ad + (j * kMxCodes >> 4), bd + j * 2,
+                                         j & 1 ? id1 : id0, sfa + (j >> 1) * 4, sfb + (j >> 1) * 4, ks != 0, issue);
                 if (issue) ptx::mma_commit(&empty[s]);
                 __syncwarp();
                 if (++s == NS) { s = 0; ph ^= 1; }
@@ -919,29 +960,60 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
             wait_bar(drained, 0, &never, status, p.wait_limit);
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // ------------------------------------------------------------ workers
-        // All eight warps round a new group's rows; warps 4-7 then move the scales
-        // and drain the accumulator.  Every worker passes the same barriers: one
-        // that has given up says so at the next, and all leave there.
-        const int w = warp - 4, wq = warp & 3;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * wq) << 16);
+    } else if (warp >= 4 && warp < 8) {
+        // -------------------------------------------------- the weights' scales
+        const uint32_t dst = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kMdColA;
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int q = (it1 - it0) * KS; q > 0 && ok; q -= 2) {  // two stages at a time: their latencies overlap
+            const int s1 = s + 1 == NS ? 0 : s + 1;
+            const uint32_t ph1 = s + 1 == NS ? ph ^ 1 : ph;
+            const bool two = q > 1;
+            ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
+                 (!two || warp_wait(&full[s1], ph1, abort_flag, status, p.wait_limit));
+            if (!ok) break;
+            uint32_t v[8], u[8];
+            weight_scales(ptx::smem_u32(ring_s + (size_t)s * kMxAScales), lane, v);
+            weight_scales(ptx::smem_u32(ring_s + (size_t)s1 * kMxAScales), lane, u);
+            ptx::tc_fence_after();
+            ptx::tmem_st_32x32b_x8(dst + (uint32_t)s * 8u, v);
+            if (two) ptx::tmem_st_32x32b_x8(dst + (uint32_t)s1 * 8u, u);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(&sf_full[s]);
+                if (two) ptx::mbar_arrive(&sf_full[s1]);
+            }
+            s = s1;
+            ph = ph1;
+            if (++s == NS) { s = 0; ph ^= 1; }
+        }
+    } else {
+        // ---------------------------------------------- rows, then accumulators
+        // Every warp here passes the same barriers: one that has given up says so at
+        // the next, and all leave there.
+        const int w = warp < 4 ? warp - 2 : warp - 6;
+        const bool drains = warp >= 8;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
-        int s = 0, group = -1;
-        uint32_t ph = 0, n = 0;
+        int group = -1;
+        uint32_t n = 0;
         bool ok = true;
         for (int it = it0; it < it1; ++it, ++n) {
             const int g = it / MT, mt = it % MT, rows = s_count[g];
-            ok = ptx::bar_red_and(kMdBarRed, kMdWorkers, ok);
-            if (!ok) break;
-            if (g != group) {  // (the MMAs of the last group have completed: acc_full below)
+            if (g != group) {
+                // warps 8-11 have seen the last item's MMAs complete
+                ok = ptx::bar_red_and(kMdBarRed, kMdRounders * 32, ok);
+                if (!ok) break;
                 group = g;
                 const int units = rows * KS;
-                for (int u0 = w; u0 < units; u0 += 8 * kMxPlanes) {
+                for (int u0 = w; u0 < units; u0 += kMdRounders * kMxPlanes) {
                     MxEight<TYPE> v[kMxPlanes];
 #pragma unroll
                     for (int i = 0; i < kMxPlanes; ++i) {
-                        const int u = u0 + 8 * i, r = u / KS, col = (u - r * KS) * 256 + lane * 8;
+                        const int u = u0 + kMdRounders * i, r = u / KS, col = (u - r * KS) * 256 + lane * 8;
                         if (u < units && col < a.n_in) {
                             const int slot = s_slots[g][r];
                             const int64_t row = a.per_slot ? slot : slot / a.k;
@@ -952,7 +1024,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                     }
 #pragma unroll
                     for (int i = 0; i < kMxPlanes; ++i) {
-                        const int u = u0 + 8 * i, r = u / KS, kp = u - r * KS;
+                        const int u = u0 + kMdRounders * i, r = u / KS, kp = u - r * KS;
                         if (u >= units) break;
                         uint32_t m = v[i].amax_bits();
                         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -968,44 +1040,45 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                     }
                 }
                 ptx::fence_proxy_async_smem();
-                ptx::bar_red_and(kMdBarRed, kMdWorkers, true);
-                if (w < 4) {
+                ptx::bar_red_and(kMdBarRed, kMdRounders * 32, true);
+                if (drains) {
                     ptx::tc_fence_after();
-                    for (int c = 0; c < 2 * KS; ++c)
-                        ptx::tmem_st_32x32b_x1(lanes + kMdColB + c * 4, s_bs[c * kMdN + (lane & 15)]);
+#pragma unroll 4
+                    for (int kp = 0; kp < KS; ++kp) {
+                        const uint32_t* q = s_bs + 2 * kp * kMdN + (lane & 15);
+                        const uint32_t v[8] = {q[0], 0u, 0u, 0u, q[kMdN], 0u, 0u, 0u};
+                        ptx::tmem_st_32x32b_x8(lanes + kMdColB + kp * 8, v);
+                    }
                     ptx::tmem_st_wait();
                     ptx::tc_fence_before();
                 }
             }
+            if (!drains) continue;
             const uint32_t buf = n & 1;
-            if (w < 4) {
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(b_full);
-                for (int ks = 0; ks < KS && ok; ++ks) {
-                    ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
-                    if (!ok) break;
-                    uint32_t v[8];
-                    weight_scales(ptx::smem_u32(ring_s + (size_t)s * kMxAScales), lane, v);
-                    ptx::tc_fence_after();
-                    ptx::tmem_st_32x32b_x8(lanes + kMdColA + (uint32_t)s * 8u, v);
-                    ptx::tmem_st_wait();
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&sf_full[s]);
-                    if (++s == NS) { s = 0; ph ^= 1; }
-                }
-            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(b_full);
+            uint32_t slots[kMdN / 2];  // two a word
+#pragma unroll
+            for (int j = 0; j < kMdN / 2; ++j) slots[j] = ((const uint32_t*)s_slots[g])[j];
+            const int m = mt * kTileM + 32 * (warp & 3) + perm_row(lane), parts = min(KT, kMxStageKt);
             ok = ok && warp_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, status, p.wait_limit);
-            if (ok && w < 4) {
+            if (ok) {
                 ptx::tc_fence_after();
-                uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(lanes + buf * kMdN, v);
+                uint32_t v[4][kMdN];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < parts) ptx::tmem_ld_32x32b_x16(lanes + buf * kMdAcc + i * kMdN, v[i]);
                 ptx::tmem_ld_wait();
-                const int m = mt * kTileM + 32 * wq + perm_row(lane);
                 if (m < L.n_out) {
 #pragma unroll
-                    for (int j = 0; j < kMdN; ++j)
-                        if (j < rows) p.out[(int64_t)s_slots[g][j] * p.out_ld + m] = __uint_as_float(v[j]);
+                    for (int j = 0; j < kMdN; ++j) {
+                        if (j >= rows) break;
+                        float r = __uint_as_float(v[0][j]);
+#pragma unroll
+                        for (int i = 1; i < 4; ++i)
+                            if (i < parts) r = __fadd_rn(r, __uint_as_float(v[i][j]));
+                        p.out[(int64_t)(slots[j / 2] >> (16 * (j & 1)) & 0xffffu) * p.out_ld + m] = r;
+                    }
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -1114,28 +1187,37 @@ moe_status launch_dependent(void (*kernel)(A), unsigned grid, int threads, size_
     return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// The kernel's shared-memory limit, set once a device.
+template <typename K>
+bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (bit & done.load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
 template <int TYPE>
 moe_status launch_place(const MxPlaceArgs& a, unsigned grid, size_t smem, cudaStream_t s) {
-    if (cudaFuncSetAttribute(mx4_place_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(34 * kRidMaxE * sizeof(int))) != cudaSuccess)
-        return MOE_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(mx4_place_kernel<TYPE>, (int)(34 * kRidMaxE * sizeof(int)), done)) return MOE_ERR_CUDA;
     return launch_dependent(mx4_place_kernel<TYPE>, grid, kMpThreads, smem, s, a);
 }
 
 template <int TYPE>
 moe_status launch_decode(const MxDecodeArgs& a, cudaStream_t s) {
-    if (cudaFuncSetAttribute(mx4_decode_kernel<TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMdSmem) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(mx4_decode_kernel<TYPE>, (int)kMdSmem, done)) return MOE_ERR_CUDA;
     const int64_t items = (int64_t)a.S * a.w.L.mt_count;  // at most: a group has a slot
     const int sms = mx_sm_count();
     return launch_dependent(mx4_decode_kernel<TYPE>, (unsigned)(items < sms ? items : sms), kMdThreads, kMdSmem, s, a);
 }
 
 moe_status launch_mx4_gemm(const Mx4Params& p, int64_t max_coltiles, cudaStream_t stream) {
-    if (cudaFuncSetAttribute(mx4_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMxSmem) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(mx4_gemm_kernel, (int)kMxSmem, done)) return MOE_ERR_CUDA;
     const int64_t units = max_coltiles * ((p.L.mt_count + p.tiles_per_unit - 1) / p.tiles_per_unit);
     const int sms = mx_sm_count();
     const unsigned grid = (unsigned)(units < sms ? units : sms);
