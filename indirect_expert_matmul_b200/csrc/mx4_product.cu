@@ -91,18 +91,19 @@ __device__ __forceinline__ int perm_row(int r) { return r ^ (r >> 3); }
 // Of the last, partial tile a k-step is one copy of its 32-row sub-blocks'
 // codes, one of its 16-row sub-block's, and the scales by sub-block (a tensor
 // copy's destination would need 128-byte alignment).
+template <int STAGE_KT>
 __device__ __forceinline__ void load_weights(const Mx4Params& p, const WLayout& L, uint8_t* codes, uint8_t* scales, int e,
                                              int mt, int ks, uint64_t* bar) {
     if (mt < p.full_tiles) {
-        ptx::mbar_arrive_expect_tx(bar, kMxACodes + kMxAScales);
-        ptx::tma_load_5d(codes, &p.codes, 0, 0, ks * kMxStageKt * 4, mt, e, bar);
-        ptx::tma_load_4d(scales, &p.scales, 0, ks * kMxStageKt * 4, mt, e, bar);
+        ptx::mbar_arrive_expect_tx(bar, STAGE_KT * (kMxCodes + 256));
+        ptx::tma_load_5d(codes, &p.codes, 0, 0, ks * STAGE_KT * 4, mt, e, bar);
+        ptx::tma_load_4d(scales, &p.scales, 0, ks * STAGE_KT * 4, mt, e, bar);
         return;
     }
-    const int kts = min(kMxStageKt, L.kt_count - ks * kMxStageKt);
+    const int kts = min(STAGE_KT, L.kt_count - ks * STAGE_KT);
     ptx::mbar_arrive_expect_tx(bar, (uint32_t)(kts * L.rows(mt) * kRowBytesMx));
     for (int j = 0; j < kts; ++j, codes += kMxCodes, scales += 256) {
-        const int kt = ks * kMxStageKt + j;
+        const int kt = ks * STAGE_KT + j;
         const uint8_t* src = p.W + L.block(e, mt, kt);
         if (p.tail_subs) ptx::tma_load_5d(codes, &p.t_codes, 0, 0, 0, kt, e, bar);
         if (p.tail_r) ptx::tma_load_5d(codes + p.tail_subs * 1024, &p.r_codes, 0, 0, 0, kt, e, bar);
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                     }
                 } else if (issue) {
                     if (i < TPU && mt < MT)
-                        load_weights(p, L, st + i * kMxACodes, st + kMxOffAS + i * kMxAScales, u.e, mt, ks, &full[s]);
+                        load_weights<kMxStageKt>(p, L, st + i * kMxACodes, st + kMxOffAS + i * kMxAScales, u.e, mt, ks, &full[s]);
                     else ptx::mbar_arrive(&full[s]);
                 }
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
@@ -286,18 +287,24 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                 const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)s * 32u;
                 const uint64_t ad = ptx::desc_k_sw32(st), bd = ptx::desc_k_sw128(st + kMxOffB);
                 const int kts = KT - ks * kMxStageKt;
-#pragma unroll
-                for (int j = 0; j < kMxStageKt; ++j) {
-                    if (j < kts) {  // address fields count 16 bytes; sums stay inside their 14 bits
+                if (issue) {
+                    // one branch for all of a stage's MMAs: a predicate on each cost ~80 cycles an MMA
+                    auto step = [&](int j) {  // address fields count 16 bytes; sums stay inside their 14 bits
                         const uint32_t id = j & 1 ? id1 : id0;
                         ptx::mma_mxf4_ss(tmem, ad + (j * kMxCodes >> 4), bd + j * 2, id, sf + (j >> 1) * 4,
-                                         sf + 16 + (j >> 1) * 8, (ks | j) != 0, issue);
+                                         sf + 16 + (j >> 1) * 8, (ks | j) != 0);
                         if (two)
                             ptx::mma_mxf4_ss(tmem + kMxBN, ad + ((kMxACodes + j * kMxCodes) >> 4), bd + j * 2, id,
-                                             sf + 8 + (j >> 1) * 4, sf + 16 + (j >> 1) * 8, (ks | j) != 0, issue);
+                                             sf + 8 + (j >> 1) * 4, sf + 16 + (j >> 1) * 8, (ks | j) != 0);
+                    };
+                    if (kts >= kMxStageKt) {
+#pragma unroll
+                        for (int j = 0; j < kMxStageKt; ++j) step(j);
+                    } else {
+                        for (int j = 0; j < kts; ++j) step(j);
                     }
+                    ptx::mma_commit(&empty[s]);
                 }
-                if (issue) ptx::mma_commit(&empty[s]);
                 __syncwarp();
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
@@ -730,17 +737,17 @@ constexpr int kMdRounders = 6;      // warps 2, 3, 8-11
 constexpr int kMdMaxSlots = 256;
 constexpr int kMdN = 16;            // columns of an accumulator
 constexpr int kMdMaxPlanes = 36;    // K up to 9216
-constexpr int kMdMaxStages = 10;
-constexpr uint32_t kMdStage = kMxACodes + kMxAScales;
+constexpr int kMdKt = 8;            // k-steps of a stage: half the copies to issue, ~450 cycles a stage
+constexpr int kMdMaxStages = 5;
+constexpr uint32_t kMdCodes = kMdKt * kMxCodes, kMdScales = kMdKt * 256, kMdStage = kMdCodes + kMdScales;
 constexpr uint32_t kMdPlane = kMdN * 128, kMdPlaneScales = 2 * kMdN * 4;
 constexpr uint32_t kMdSmem = 211 * 1024;
 // Tensor memory: two times four accumulators (MMAs into one accumulator wait for
-// one another, ~170 cycles each however narrow; k-step j of a stage goes to
-// accumulator j and the drain adds the four), the stages' A scales (8 columns
-// each), the B scales of all of K (4 columns per 128 values, 16 rows take the
+// one another; k-step j of a stage goes to accumulator j % 4 and the drain adds
+// the four), the stages' A scales (16 columns each), the B scales of all of K (4 columns per 128 values, 16 rows take the
 // first).
-constexpr uint32_t kMdAcc = kMxStageKt * kMdN;
-constexpr uint32_t kMdColA = 2 * kMdAcc, kMdColB = kMdColA + 8 * kMdMaxStages;
+constexpr uint32_t kMdAcc = 4 * kMdN;
+constexpr uint32_t kMdColA = 2 * kMdAcc, kMdColB = kMdColA + 2 * kMdKt * kMdMaxStages;
 static_assert(kMdColA % 4 == 0 && kMdColB % 4 == 0 && kMdColB + 8 * kMdMaxPlanes <= 512, "tensor memory");
 constexpr int kMdBarRed = 1;  // named barrier of the workers
 
@@ -767,12 +774,12 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
     const Mx4Params& p = a.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WLayout L = p.L;
-    const int MT = L.mt_count, KT = L.kt_count, KS = (KT + kMxStageKt - 1) / kMxStageKt, NS = a.stages, S = a.S;
+    const int MT = L.mt_count, KT = L.kt_count, planes = (KT + 3) / 4, KS = (KT + kMdKt - 1) / kMdKt, NS = a.stages, S = a.S;
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_dyn + 1023) & ~(uintptr_t)1023);
     uint8_t* s_b = smem;                                        // [plane][16][128]
-    uint8_t* ring = smem + (size_t)KS * kMdPlane;               // codes of the stages
-    uint8_t* ring_s = ring + (size_t)NS * kMxACodes;            // scales of the stages
-    uint32_t* s_bs = (uint32_t*)(ring_s + (size_t)NS * kMxAScales);  // [K / 128][16]
+    uint8_t* ring = smem + (size_t)planes * kMdPlane;           // codes of the stages
+    uint8_t* ring_s = ring + (size_t)NS * kMdCodes;             // scales of the stages
+    uint32_t* s_bs = (uint32_t*)(ring_s + (size_t)NS * kMdScales);  // [K / 128][16]
     uint64_t* full = s_bar;
     uint64_t* sf_full = full + kMdMaxStages;
     uint64_t* empty = sf_full + kMdMaxStages;
@@ -783,6 +790,14 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
     volatile int* abort_flag = &s_abort;
     int* status = p.hdr + kHdrStatus;
 
+    if (tid == 0) {
+        if (p.full_tiles) {
+            ptx::prefetch_tensormap(&p.codes);
+            ptx::prefetch_tensormap(&p.scales);
+        }
+        if (p.tail_subs) ptx::prefetch_tensormap(&p.t_codes);
+        if (p.tail_r) ptx::prefetch_tensormap(&p.r_codes);
+    }
     // (warp 0 goes straight for the ids)
     if (warp == 2) {
         if (lane < NS) {
@@ -907,8 +922,8 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                 if (!ok) break;
                 if (!((int)blockIdx.x == p.stall_cta && q == p.stall_stage)) {
                     if (issue)
-                        load_weights(p, L, ring + (size_t)s * kMxACodes, ring_s + (size_t)s * kMxAScales, e, mt, ks,
-                                     &full[s]);
+                        load_weights<kMdKt>(p, L, ring + (size_t)s * kMdCodes, ring_s + (size_t)s * kMdScales, e, mt, ks,
+                                            &full[s]);
                     used |= 1u << s;
                     par = (par & ~(1u << s)) | (ph << s);
                 }
@@ -937,16 +952,25 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                 ok = warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint64_t ad = ptx::desc_k_sw32(ring_a + (uint32_t)s * kMxACodes);
-                const uint64_t bd = ptx::desc_k_sw128(b_a + (uint32_t)ks * kMdPlane);
-                const uint32_t sfa = tmem + kMdColA + (uint32_t)s * 8u, sfb = tmem + kMdColB + (uint32_t)ks * 8u;
-                const int kts = KT - ks * kMxStageKt;
+                const uint64_t ad = ptx::desc_k_sw32(ring_a + (uint32_t)s * kMdCodes);
+                const uint64_t bd = ptx::desc_k_sw128(b_a + (uint32_t)ks * (kMdKt / 4 * kMdPlane));
+                const uint32_t sfa = tmem + kMdColA + (uint32_t)s * (2 * kMdKt);
+                const uint32_t sfb = tmem + kMdColB + (uint32_t)ks * (2 * kMdKt);
+                const int kts = KT - ks * kMdKt;
+                if (issue) {
+                    auto step = [&](int j) {
+                        ptx::mma_mxf4_ss(tmem + buf * kMdAcc + (j & 3) * kMdN, ad + (j * kMxCodes >> 4),
+                                         bd + ((j >> 2) * kMdPlane >> 4) + (j & 3) * 2, j & 1 ? id1 : id0,
+                                         sfa + (j >> 1) * 4, sfb + (j >> 1) * 4, ks != 0 || j > 3);
+                    };
+                    if (kts >= kMdKt) {
 #pragma unroll
-                for (int j = 0; j < kMxStageKt; ++j)
-                    if (j < kts)
-                        ptx::mma_mxf4_ss(tmem + buf * kMdAcc + j * kMdN, ad + (j * kMxCodes >> 4), bd + j * 2,
-                                         j & 1 ? id1 : id0, sfa + (j >> 1) * 4, sfb + (j >> 1) * 4, ks != 0, issue);
-                if (issue) ptx::mma_commit(&empty[s]);
+                        for (int j = 0; j < kMdKt; ++j) step(j);
+                    } else {
+                        for (int j = 0; j < kts; ++j) step(j);
+                    }
+                    ptx::mma_commit(&empty[s]);
+                }
                 __syncwarp();
                 if (++s == NS) { s = 0; ph ^= 1; }
             }
@@ -966,28 +990,20 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int q = (it1 - it0) * KS; q > 0 && ok; q -= 2) {  // two stages at a time: their latencies overlap
-            const int s1 = s + 1 == NS ? 0 : s + 1;
-            const uint32_t ph1 = s + 1 == NS ? ph ^ 1 : ph;
-            const bool two = q > 1;
-            ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
-                 (!two || warp_wait(&full[s1], ph1, abort_flag, status, p.wait_limit));
+        for (int q = (it1 - it0) * KS; q > 0; --q) {
+            ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
             if (!ok) break;
-            uint32_t v[8], u[8];
-            weight_scales(ptx::smem_u32(ring_s + (size_t)s * kMxAScales), lane, v);
-            weight_scales(ptx::smem_u32(ring_s + (size_t)s1 * kMxAScales), lane, u);
+            uint32_t v[2][8];
+            const uint32_t src = ptx::smem_u32(ring_s + (size_t)s * kMdScales);
+            weight_scales(src, lane, v[0]);
+            weight_scales(src + kMxAScales, lane, v[1]);
             ptx::tc_fence_after();
-            ptx::tmem_st_32x32b_x8(dst + (uint32_t)s * 8u, v);
-            if (two) ptx::tmem_st_32x32b_x8(dst + (uint32_t)s1 * 8u, u);
+            ptx::tmem_st_32x32b_x8(dst + (uint32_t)s * (2 * kMdKt), v[0]);
+            ptx::tmem_st_32x32b_x8(dst + (uint32_t)s * (2 * kMdKt) + 8u, v[1]);
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(&sf_full[s]);
-                if (two) ptx::mbar_arrive(&sf_full[s1]);
-            }
-            s = s1;
-            ph = ph1;
+            if (lane == 0) ptx::mbar_arrive(&sf_full[s]);
             if (++s == NS) { s = 0; ph ^= 1; }
         }
     } else {
@@ -1008,12 +1024,12 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                 ok = ptx::bar_red_and(kMdBarRed, kMdRounders * 32, ok);
                 if (!ok) break;
                 group = g;
-                const int units = rows * KS;
+                const int units = rows * planes;
                 for (int u0 = w; u0 < units; u0 += kMdRounders * kMxPlanes) {
                     MxEight<TYPE> v[kMxPlanes];
 #pragma unroll
                     for (int i = 0; i < kMxPlanes; ++i) {
-                        const int u = u0 + kMdRounders * i, r = u / KS, col = (u - r * KS) * 256 + lane * 8;
+                        const int u = u0 + kMdRounders * i, r = u / planes, col = (u - r * planes) * 256 + lane * 8;
                         if (u < units && col < a.n_in) {
                             const int slot = s_slots[g][r];
                             const int64_t row = a.per_slot ? slot : slot / a.k;
@@ -1024,7 +1040,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                     }
 #pragma unroll
                     for (int i = 0; i < kMxPlanes; ++i) {
-                        const int u = u0 + kMdRounders * i, r = u / KS, kp = u - r * KS;
+                        const int u = u0 + kMdRounders * i, r = u / planes, kp = u - r * planes;
                         if (u >= units) break;
                         uint32_t m = v[i].amax_bits();
                         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -1044,7 +1060,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                 if (drains) {
                     ptx::tc_fence_after();
 #pragma unroll 4
-                    for (int kp = 0; kp < KS; ++kp) {
+                    for (int kp = 0; kp < planes; ++kp) {
                         const uint32_t* q = s_bs + 2 * kp * kMdN + (lane & 15);
                         const uint32_t v[8] = {q[0], 0u, 0u, 0u, q[kMdN], 0u, 0u, 0u};
                         ptx::tmem_st_32x32b_x8(lanes + kMdColB + kp * 8, v);
@@ -1060,7 +1076,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
             uint32_t slots[kMdN / 2];  // two a word
 #pragma unroll
             for (int j = 0; j < kMdN / 2; ++j) slots[j] = ((const uint32_t*)s_slots[g])[j];
-            const int m = mt * kTileM + 32 * (warp & 3) + perm_row(lane), parts = min(KT, kMxStageKt);
+            const int m = mt * kTileM + 32 * (warp & 3) + perm_row(lane), parts = min(KT, 4);
             ok = ok && warp_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, status, p.wait_limit);
             if (ok) {
                 ptx::tc_fence_after();
@@ -1134,7 +1150,7 @@ bool encode(CUtensorMap* m, const uint8_t* base, int rank, const cuuint64_t* dim
 // is 1088 bytes: 32 rows of 32 code bytes (eight lines of 128), then 64 scale
 // bytes; a full tile's k-steps and sub-blocks follow one another, so they are
 // one dimension.
-bool plan_weights(Mx4Params& p, int n_experts) {
+bool plan_weights(Mx4Params& p, int n_experts, int stage_kt) {
     const WLayout& L = p.L;
     const cuuint64_t sub = kSubRows * kRowBytesMx, ex = (cuuint64_t)L.expert_bytes, KT = (cuuint64_t)L.kt_count;
     p.full_tiles = L.n_out_pad / kTileM;
@@ -1145,10 +1161,10 @@ bool plan_weights(Mx4Params& p, int n_experts) {
         const cuuint64_t tile = kTileM * KT * kRowBytesMx;
         const cuuint64_t cd[5] = {128, 8, KT * 4, (cuuint64_t)p.full_tiles, (cuuint64_t)n_experts};
         const cuuint64_t cs[4] = {128, sub, tile, ex};
-        const cuuint32_t cb[5] = {128, 8, kMxStageKt * 4, 1, 1};
+        const cuuint32_t cb[5] = {128, 8, (cuuint32_t)stage_kt * 4, 1, 1};
         const cuuint64_t sd[4] = {64, KT * 4, (cuuint64_t)p.full_tiles, (cuuint64_t)n_experts};
         const cuuint64_t ss[3] = {sub, tile, ex};
-        const cuuint32_t sb[4] = {64, kMxStageKt * 4, 1, 1};
+        const cuuint32_t sb[4] = {64, (cuuint32_t)stage_kt * 4, 1, 1};
         if (!encode(&p.codes, p.W, 5, cd, cs, cb, CU_TENSOR_MAP_SWIZZLE_128B) ||
             !encode(&p.scales, p.W + kSubRows * 32, 4, sd, ss, sb, CU_TENSOR_MAP_SWIZZLE_NONE))
             return false;
@@ -1251,7 +1267,9 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     Mx4Params p = {};
     p.W = (const uint8_t*)W_prepared;
     p.L = WLayout(n_out, n_in, MOE_MXFP4);
-    if (!plan_weights(p, n_experts)) return MOE_ERR_CUDA;
+    const int planes = (n_in + 255) / 256;
+    const bool few = S <= kMdMaxSlots && planes <= kMdMaxPlanes;
+    if (!plan_weights(p, n_experts, few ? kMdKt : kMxStageKt)) return MOE_ERR_CUDA;
     p.out = dst;
     p.out_ld = n_out;
     p.hdr = hdr;
@@ -1259,8 +1277,7 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     p.stall_cta = -1;
     long long limit = 0;
     if (testing_stall_state(&p.stall_cta, &p.stall_stage, &limit)) p.wait_limit = limit;
-    const int planes = (n_in + 255) / 256;
-    if (S <= kMdMaxSlots && planes <= kMdMaxPlanes) {
+    if (few) {
         MxDecodeArgs a = {};
         a.w = p;
         a.ids = ids;

@@ -117,6 +117,11 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// Fetch a tensor map (a __grid_constant__ parameter) ahead of its first copy.
+__device__ __forceinline__ void prefetch_tensormap(const void* tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 // One box of a 4-D tensor map (coordinates innermost first) into dst, completing
 // its bytes on bar.  No multicast: the box lands in this CTA's shared memory.
 __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3,
@@ -190,17 +195,14 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 // D(tmem) (+)= (A * scales) (B * scales)^T, kind::mxf4: both operands packed
 // E2M1 codes in shared memory, one E8M0 scale per 32 values of each row in
 // tensor memory (sfa, sfb; layout at idesc_mxf4), fp32 accumulation.  K = 64.
-// Issued by the lane whose `issue` is non-zero; the warp stays converged, so
-// that the operands are computed in uniform registers.
 __device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t issue) {
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue)
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 // One lane of a converged warp: non-zero in exactly one lane, always the same.
