@@ -171,10 +171,13 @@ def _call(what, dev, fn, *args):
         raise MoeError(rc, what)
 
 
+_Tensor = torch.Tensor
+
+
 def _at(t, name, dtype, numel, dev):
     """The address of a tensor that _need accepts (the checks in one test: a
     small call's time is the host's)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.is_contiguous() \
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev.index and t.is_contiguous() \
             and t.numel() >= numel:
         return t.data_ptr()
     return _need(t, name, dtype, numel, dev).data_ptr()
@@ -322,22 +325,24 @@ def mul_mat_id_mx4(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None,
     MXFP4 blocks by the call as mxfp4_quantize rounds.
 
     Arguments, workspace and errors as for mul_mat_id."""
-    _cuda(x, "x")
-    if x.dtype not in _XTYPE:
+    _gpu(x, "x")
+    dtype, dev = x.dtype, x.device
+    xt = _XTYPE.get(dtype)
+    if xt is None:
         raise ValueError("x must be bfloat16, float16 or float32")
-    dev = x.device
-    _cuda(ids, "ids", torch.int32, dev)
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a [T][k] tensor")
     T, k = ids.shape
-    xt, m, L = _XTYPE[x.dtype], _MODE[mode], _L()
+    S, m, L = T * k, _MODE[mode], _L()
     own_ws = ws is None
     if own_ws:
-        ws = workspace(T, k, n_experts, n_in, x_dtype=x.dtype, device=dev)
+        ws = workspace(T, k, n_experts, n_in, x_dtype=dtype, device=dev)
     if out is None:
         out = torch.empty((T, k, n_out), dtype=torch.float32, device=dev)
     _call("moe_mul_mat_id_mx4", dev, L.moe_mul_mat_id_mx4,
-          _at(W, "W", torch.uint8, _prepared_bytes(MXFP4, n_experts, n_out, n_in), dev),
-          n_experts, n_out, n_in, _at(x, "x", x.dtype, (T if m == BROADCAST else T * k) * n_in, dev), xt,
-          ids.data_ptr(), T, k, m, _at(out, "out", torch.float32, T * k * n_out, dev),
+          _at(W, "W", torch.uint8, _prepared_bytes(MXFP4, n_experts, n_out, n_in), dev), n_experts, n_out, n_in,
+          _at(x, "x", dtype, (T if m == BROADCAST else S) * n_in, dev), xt, _at(ids, "ids", torch.int32, S, dev), T, k,
+          m, _at(out, "out", torch.float32, S * n_out, dev),
           _at(ws, "ws", torch.uint8, _workspace_bytes(T, k, n_experts, n_in, xt), dev))
     if own_ws:
         _chk(get_status(ws), "moe_mul_mat_id_mx4 (device status)")
@@ -473,14 +478,13 @@ def route_scored_backward(logits, ids, dweights, score="sigmoid", normalize=True
         raise ValueError("logits must be a [T][E] tensor of float32, bfloat16 or float16")
     T, E, ld = _rows(logits, "logits")
     dev = logits.device
-    _cuda(ids, "ids", torch.int32, dev)
-    if ids.dim() != 2 or ids.shape[0] != T:
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError("ids must be [T][k]")
     k = ids.shape[1]
     if out is None:
         out = torch.empty((T, E), dtype=logits.dtype, device=dev)
     _call("moe_route_scored_backward", dev, _L().moe_route_scored_backward, logits.data_ptr(), _XTYPE[logits.dtype],
-          ld, ids.data_ptr(), _at(dweights, "dweights", torch.float32, T * k, dev), T, E, k, _SCORE[score],
+          ld, _at(ids, "ids", torch.int32, T * k, dev), _at(dweights, "dweights", torch.float32, T * k, dev), T, E, k, _SCORE[score],
           1 if normalize else 0, scale, _at(out, "out", logits.dtype, T * E, dev))
     return out
 
@@ -490,14 +494,14 @@ def combine_backward(dy, dst, weights, need_ddst=True, dweights=None, ddst=None)
     dst: float32 [T][k][n] (or [T*k][n]); weights: float32 [T][k].  Returns
     (dweights [T][k], ddst of dst's shape, or None without `need_ddst`); the
     gradient of the shared term is dy itself.  ddst may be dst."""
-    _cuda(dst, "dst", torch.float32)
+    _gpu(dst, "dst")
     dev = dst.device
-    _cuda(weights, "weights", torch.float32, dev)
-    if weights.dim() != 2:
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 2:
         raise ValueError("weights must be [T][k]")
     T, k = weights.shape
     n = dst.shape[-1]
-    if dst.numel() != T * k * n:
+    S = T * k
+    if dst.numel() != S * n:
         raise ValueError("dst must hold n_tokens*k rows of n")
     if dweights is None:
         dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
@@ -506,8 +510,9 @@ def combine_backward(dy, dst, weights, need_ddst=True, dweights=None, ddst=None)
     elif ddst is None:
         ddst = torch.empty_like(dst)
     _call("moe_combine_backward", dev, _L().moe_combine_backward, _at(dy, "dy", torch.float32, T * n, dev),
-          dst.data_ptr(), weights.data_ptr(), T, k, n, _at(dweights, "dweights", torch.float32, T * k, dev),
-          None if ddst is None else _at(ddst, "ddst", torch.float32, T * k * n, dev))
+          _at(dst, "dst", torch.float32, S * n, dev), _at(weights, "weights", torch.float32, S, dev), T, k, n,
+          _at(dweights, "dweights", torch.float32, S, dev),
+          None if ddst is None else _at(ddst, "ddst", torch.float32, S * n, dev))
     return dweights, ddst
 
 
