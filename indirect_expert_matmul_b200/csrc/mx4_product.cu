@@ -2,10 +2,8 @@
 //   dst[t][s] = W[ids[t][s]] . Q(x[t] or x[t][s]),
 // Q rounding every 32 consecutive values to one E8M0 scale and E2M1 codes.
 //
-// Quantising gather: each row is rounded once and its codes go to the tile rows
-// of every slot that reads it: [K plane of 256 values][row][128 bytes], 16-byte
-// chunk c at c ^ (row % 8) (the 128-byte swizzle); the scales of 128 values of
-// a row are one word of [K / 128][row].
+// Rounding: each source row is rounded once to a row of codes (two to a byte, K
+// order) and a row of scale words (four scale bytes for 128 values).
 //
 // Grouped GEMM (tcgen05 kind::mxf4, block scales): a CTA takes units of (up to
 // 192 sorted rows of one expert) x (one or two 128-row weight tiles) and streams
@@ -41,7 +39,8 @@ bool testing_stall_state(int* cta, int* stage, long long* limit_cycles);
 namespace {
 
 // ----------------------------------------------------------------- geometry
-constexpr int kMxThreads = 512;
+constexpr int kMxThreads = 640;
+constexpr int kMxGather = 128;    // threads that gather the rows' codes and scales
 constexpr int kMxBN = kGemmBN;    // sorted rows (columns of the accumulator) of a unit
 constexpr int kMxStageKt = 4;     // 64-value k-steps of a stage
 constexpr int kMxStages = 3;
@@ -49,7 +48,7 @@ constexpr uint32_t kMxCodes = kTileM * 32;                 // codes of a tile's 
 constexpr uint32_t kMxACodes = kMxStageKt * kMxCodes;      // 16384
 constexpr uint32_t kMxAScales = kMxStageKt * kTileM * 2;   // 1024
 constexpr uint32_t kMxB = kMxBN * 128;                     // 24576
-constexpr uint32_t kMxBScales = 2 * kMxBN * 4;             // 1536
+constexpr uint32_t kMxBScales = kMxBN * 8;                 // 1536: a row's two words
 constexpr uint32_t kMxStageBytes = 2 * kMxACodes + kMxB + 2 * kMxAScales + kMxBScales;
 static_assert(kMxStageBytes % 1024 == 512, "stages are padded to the swizzle's 1024 bytes below");
 constexpr uint32_t kMxStagePitch = (kMxStageBytes + 1023) / 1024 * 1024;
@@ -71,11 +70,11 @@ struct Mx4Params {
     int tail_subs, tail_r;          // last tile: number of 32-row sub-blocks, of 16-row ones (0 or 1)
     int tiles_per_unit;             // 1 or 2
     int n_groups;
-    const int32_t *bounds, *ntile_prefix, *pad_start;
-    const uint8_t* B;               // codes [plane][rows_pad][128]
-    const uint32_t* BS;             // scales [K / 128][scale_ld]
-    int64_t rows_pad, scale_ld;
-    const int32_t* dst_rows;
+    const int32_t *bounds, *ntile_prefix;
+    const uint8_t* B;               // rounded source rows: codes, b_pitch bytes a row
+    const uint8_t* BS;              // and scales, bs_pitch bytes a row
+    int b_pitch, bs_pitch;
+    const int32_t *src_rows, *dst_rows;  // source row and row of dst of a sorted position
     float* out;
     int out_ld;
     int* hdr;
@@ -132,14 +131,13 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 struct MxTile {
-    int e, mu, p0, n, p0pad;
+    int e, mu, p0, n;
 };
 
 __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
     extern __shared__ uint8_t smem_dyn[];
     __shared__ int s_prefix[kMxSmemGroups + 1];
     __shared__ int s_bounds[kMxSmemGroups + 1];
-    __shared__ int s_pad[kMxSmemGroups + 1];
     __shared__ __align__(16) int s_rows[8][kMxBN];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total;
@@ -162,7 +160,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
 
     if (tid == 0) {
         for (int i = 0; i < kMxStages; ++i) {
-            ptx::mbar_init(&full[i], 3);
+            ptx::mbar_init(&full[i], 2 + kMxGather);
             ptx::mbar_init(&sf_full[i], 4);
             ptx::mbar_init(&empty[i], 1);
         }
@@ -186,7 +184,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         for (int i = tid; i <= p.n_groups; i += kMxThreads) {
             s_prefix[i] = p.ntile_prefix[i];
             s_bounds[i] = p.bounds[i];
-            s_pad[i] = p.pad_start[i];
         }
     ptx::tc_fence_before();
     __syncthreads();
@@ -199,7 +196,6 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         r.mu = t - q * MU;
         const int* pre = in_smem ? s_prefix : p.ntile_prefix;
         const int* bnd = in_smem ? s_bounds : p.bounds;
-        const int* pad = in_smem ? s_pad : p.pad_start;
         int lo = 0, hi = p.n_groups;  // pre[lo] <= q < pre[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -208,62 +204,95 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         r.e = lo;
         const int j = q - pre[lo];
         r.p0 = bnd[lo] + j * kMxBN;
-        r.p0pad = pad[lo] + j * kMxBN;
         r.n = min(kMxBN, bnd[lo + 1] - r.p0);
         return r;
     };
 
-    if (warp == 0 || warp == 2 || warp == 3) {
-        // ------------------------------------------------------------ copies
-        // Warps 0 and 2: the codes and scales of the unit's first and second
-        // weight tile; warp 3: the rows' codes and scales.  One thread issuing all
-        // of a stage's copies needed ~1300 cycles for it, twice the MMAs' time.
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------------------ weights
+        // The codes and scales of the unit's first (warp 0) and second weight tile.
+        // One thread issuing all of a stage's copies needed ~1300 cycles for it, twice
+        // the MMAs' time.
         const uint32_t issue = ptx::elect_one();
-        const int i = warp >> 1;  // weight tile of warps 0 and 2
-        int s = 0, q = 0;
+        const int i = warp >> 1;
+        int s = 0;
         uint32_t ph = 0, used = 0, par = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
             const MxTile u = unit(t);
-            const uint32_t n16 = (uint32_t)(u.n + 15) & ~15u;
             const int mt = u.mu * TPU + i;
-            const uint8_t* bsrc = p.B + (size_t)u.p0pad * 128u;
-            const uint32_t* ssrc = p.BS + u.p0pad;
-            for (int ks = 0; ks < KS; ++ks, ++q) {
+            for (int ks = 0; ks < KS; ++ks) {
                 ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 uint8_t* st = smem + s * kMxStagePitch;
-                const int kts = min(kMxStageKt, KT - ks * kMxStageKt), halves = (kts + 1) / 2;
-                if (warp == 3) {
-                    const bool stalled = (int)blockIdx.x == p.stall_cta && q == p.stall_stage;
-                    if (issue && !stalled) {
-                        ptx::mbar_arrive_expect_tx(&full[s], n16 * 128u + halves * n16 * 4u);
-                        ptx::bulk_g2s(st + kMxOffB, bsrc, n16 * 128u, &full[s]);
-                        ptx::bulk_g2s(st + kMxOffBS, ssrc, n16 * 4u, &full[s]);
-                        if (halves == 2)
-                            ptx::bulk_g2s(st + kMxOffBS + kMxBN * 4, ssrc + p.scale_ld, n16 * 4u, &full[s]);
-                    }
-                    bsrc += (size_t)p.rows_pad * 128u;
-                    ssrc += 2 * p.scale_ld;
-                    if (!stalled) {
-                        used |= 1u << s;
-                        par = (par & ~(1u << s)) | (ph << s);
-                    }
-                } else if (issue) {
+                if (issue) {
                     if (i < TPU && mt < MT)
-                        load_weights<kMxStageKt>(p, L, st + i * kMxACodes, st + kMxOffAS + i * kMxAScales, u.e, mt, ks, &full[s]);
+                        load_weights<kMxStageKt>(p, L, st + i * kMxACodes, st + kMxOffAS + i * kMxAScales, u.e, mt, ks,
+                                                 &full[s]);
                     else ptx::mbar_arrive(&full[s]);
                 }
+                used |= 1u << s;
+                par = (par & ~(1u << s)) | (ph << s);
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
         }
         // let every copy issued land before the CTA can exit (bounded): a stage
-        // completes when all three warps' copies have
-        if (warp == 3) {
-            volatile int never = 0;
-            for (int j = 0; j < kMxStages; ++j)
-                if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, p.wait_limit);
+        // completes when all warps' copies have
+        volatile int never = 0;
+        for (int j = 0; j < kMxStages; ++j)
+            if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, p.wait_limit);
+    } else if (warp >= 16) {
+        // --------------------------------------------------------------- rows
+        // The unit's rows lie anywhere in the rounded source rows (a token's row serves
+        // k experts): eight lanes copy the 128 bytes of a row's stage, four rows an
+        // instruction, into the 128-byte swizzle the MMA reads.  (Copying every row to
+        // a place in its expert's order first cost 117 MB written and read again in
+        // the 4096-token gate product.)  The copies are generic-proxy writes: the scale
+        // warps fence them for the MMAs.
+        const int g = warp - 16, c = lane & 7;
+        const uint32_t smem_a = ptx::smem_u32(smem);
+        int s = 0, q = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const MxTile u = unit(t);
+            const uint8_t* src[kMxBN / 16];  // of rows 16 i + 4 g + lane / 8
+            const uint8_t* ssrc[2];          // of rows 48 g + lane, 48 g + 32 + lane
+#pragma unroll
+            for (int i = 0; i < kMxBN / 16; ++i) {
+                const int r = 16 * i + 4 * g + (lane >> 3);
+                src[i] = p.B + (r < u.n ? (int64_t)__ldg(p.src_rows + u.p0 + r) * p.b_pitch + c * 16 : 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 48 * g + 32 * i + lane;
+                ssrc[i] = p.BS + (r < u.n && (i == 0 || lane < 16)
+                                      ? (int64_t)__ldg(p.src_rows + u.p0 + r) * p.bs_pitch : 0);
+            }
+            for (int ks = 0; ks < KS; ++ks, ++q) {
+                ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                if (!((int)blockIdx.x == p.stall_cta && q == p.stall_stage)) {
+                    const uint32_t st = smem_a + s * kMxStagePitch;
+                    const bool in_k = ks * 128 + c * 16 < p.b_pitch;
+#pragma unroll
+                    for (int i = 0; i < kMxBN / 16; ++i) {
+                        const int r = 16 * i + 4 * g + (lane >> 3);
+                        if (r < u.n && in_k)
+                            ptx::cp_async16(st + kMxOffB + r * 128 + ((c ^ (r & 7)) << 4), src[i] + ks * 128);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 48 * g + 32 * i + lane;
+                        if (r < u.n && (i == 0 || lane < 16))
+                            ptx::cp_async8(st + kMxOffBS + r * 8, ssrc[i] + ks * 8);
+                    }
+                    ptx::cp_async_arrive(&full[s]);
+                }
+                if (++s == kMxStages) { s = 0; ph ^= 1; }
+            }
         }
+        ptx::cp_async_wait_all();
     } else if (warp == 1) {
         // -------------------------------------------------------------- MMAs
         const uint32_t issue = ptx::elect_one(), smem_a = ptx::smem_u32(smem);
@@ -332,15 +361,17 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                 ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS);
-                const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 4;
+                const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 8;
+                ptx::fence_proxy_async_smem();  // the gathered rows, for the MMAs
                 uint32_t v[32];
                 weight_scales(as, lane, v);
                 weight_scales(as + kMxAScales, lane, v + 8);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        v[16 + h * 8 + c] = c < kMxBN / 32 ? ptx::lds32(bs + h * (kMxBN * 4) + c * 128) : 0u;
+                for (int c = 0; c < 8; ++c) {
+                    const uint2 w = c < kMxBN / 32 ? ptx::lds64(bs + c * 256) : make_uint2(0u, 0u);
+                    v[16 + c] = w.x;
+                    v[24 + c] = w.y;
+                }
                 ptx::tc_fence_after();
                 ptx::tmem_st_32x32b_x32(dst + (uint32_t)s * 32u, v);
                 ptx::tmem_st_wait();
@@ -350,7 +381,7 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
         }
-    } else if (warp >= 8) {
+    } else if (warp >= 8 && warp < 16) {
         // ---------------------------------------------------------- epilogue
         // Warps 8-11 drain the first tile's accumulator, 12-15 the second's.
         const int wq = warp & 3, i = (warp - 8) >> 2;
@@ -410,13 +441,12 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
 }
 
 // -------------------------------------------------------- quantising gather
-// Where the rounded rows go: codes [plane of 256 values][row][128 bytes], the
-// 16-byte chunk of block c at c ^ (row % 8); scales [128 values][row], a word
-// of four scale bytes.
+// Where the rounded rows go, in the order of the source rows: 32 code bytes a
+// 64-value k-step (padded with zeros), and two scale words a 256-value plane.
 struct MxRows {
     uint8_t* codes;
-    uint32_t* scales;
-    int64_t rows_pad, scale_ld;
+    uint8_t* scales;
+    int pitch, scale_pitch;
 };
 
 // Eight consecutive values as they lie in memory: maximum and codes.
@@ -475,10 +505,10 @@ struct MxEight {
 constexpr int kMxPlanes = 4;  // planes of a row a warp has in flight
 
 // Planes kp0 .. kp0 + 3 (256 values each) of source row r by one warp, eight
-// values a lane, four lanes a block, to the tile rows prow[0 .. copies).
+// values a lane, four lanes a block.
 template <int TYPE>
 __device__ __forceinline__ void round_planes(const void* __restrict__ x, int64_t r, int n_in, int kp0, int planes,
-                                             const int32_t* prow, int copies, const MxRows& o, int lane) {
+                                             const MxRows& o, int lane) {
     constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
     const int col = kp0 * 256 + lane * 8;
     const char* src = (const char*)x + (r * n_in + col) * esz;
@@ -488,49 +518,37 @@ __device__ __forceinline__ void round_planes(const void* __restrict__ x, int64_t
         if (col + i * 256 < n_in) v[i].load(src + i * 256 * esz);
         else v[i].zero();
     }
-    uint32_t w[kMxPlanes], sw[kMxPlanes];
+    uint8_t* codes = o.codes + r * o.pitch + kp0 * 128 + lane * 4;
+    const int left = o.pitch - kp0 * 128 - lane * 4;
+    uint32_t word = 0u;  // lanes 0-7: the scale word of half lane % 2 of plane lane / 2
 #pragma unroll
     for (int i = 0; i < kMxPlanes; ++i) {
         uint32_t m = v[i].amax_bits();
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const uint32_t X = mx_scale_byte(m);
-        w[i] = X == 255u ? 0u : v[i].codes(mx_inv_scale(X));
-        sw[i] = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
-        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 4);
-        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 8);
+        const uint32_t w = X == 255u ? 0u : v[i].codes(mx_inv_scale(X));
+        if (i * 128 < left) *(uint32_t*)(codes + i * 128) = w;
+        uint32_t sw = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
+        sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
+        sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
+        const uint32_t half = __shfl_sync(0xffffffffu, sw, (lane & 1) * 16);
+        if ((lane >> 1) == i) word = half;
     }
-    const size_t pitch = (size_t)o.rows_pad * 128u;
-    uint8_t* plane = o.codes + (size_t)kp0 * pitch + (lane & 3) * 4;
-    uint32_t* sp = o.scales + (size_t)(2 * kp0 + (lane >> 4)) * o.scale_ld;
-    const bool sc = (lane & 15) == 0;
-    for (int j = 0; j < copies; ++j) {
-        const uint32_t pr = (uint32_t)prow[j];
-        uint8_t* c = plane + ((size_t)pr * 128u + (((uint32_t)(lane >> 2) ^ (pr & 7u)) << 4));
-        uint32_t* q = sp + pr;
-#pragma unroll
-        for (int i = 0; i < kMxPlanes; ++i) {
-            if (kp0 + i < planes) *(uint32_t*)c = w[i];
-            if (sc && col + i * 256 < n_in) *q = sw[i];
-            c += pitch;
-            q += 2 * o.scale_ld;
-        }
-    }
+    if (lane < 2 * kMxPlanes && kp0 + (lane >> 1) < planes)
+        *(uint32_t*)(o.scales + r * o.scale_pitch + kp0 * 8 + lane * 4) = word;
 }
 
-// After the general row-id pass: one warp per source row (broadcast: a token,
-// whose codes go to the tile rows of its k slots; per slot: one slot).
+// After the general row-id pass: one warp per source row.
 template <int TYPE>
 __global__ void __launch_bounds__(256)
-mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restrict__ slot_prow, int copies,
-                  int64_t n_rows, MxRows o, const int* hdr) {
+mx4_round_kernel(const void* __restrict__ x, int n_in, int64_t n_rows, MxRows o, const int* hdr) {
     if (read_status(hdr + kHdrStatus) != 0) return;
     const int lane = threadIdx.x & 31;
     const int planes = (n_in + 255) / 256;
     const int64_t nw = (int64_t)gridDim.x * (blockDim.x / 32);
     for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < n_rows; r += nw)
-        for (int kp = 0; kp < planes; kp += kMxPlanes)
-            round_planes<TYPE>(x, r, n_in, kp, planes, slot_prow + r * copies, copies, o, lane);
+        for (int kp = 0; kp < planes; kp += kMxPlanes) round_planes<TYPE>(x, r, n_in, kp, planes, o, lane);
 }
 
 // ------------------------------------------- row ids and gather in two launches
@@ -539,7 +557,7 @@ mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restric
 // of the skewed 8192-token one): G CTAs count their tokens' slots by expert;
 // then each CTA sums the counts before its own (the place of its first slot of
 // every expert, the tables' prefixes), ranks its slots in slot order - the same
-// stable counting sort - and rounds its rows straight into their tile rows.
+// stable counting sort - and rounds its rows.
 // The second launch starts while the first runs and fetches its rows into L2.
 constexpr int kMpThreads = 1024;
 constexpr int64_t kMpPrefetch = 512 * 1024;
@@ -570,7 +588,7 @@ struct MxPlaceArgs {
     int64_t T;
     int k, E, per_slot;
     const int32_t* counts;
-    int32_t *bounds, *ntile_prefix, *pad_start, *ids_dst, *slot_prow;
+    int32_t *bounds, *ntile_prefix, *ids_src, *ids_dst;
     int* hdr;
     MxRows rows;
 };
@@ -598,8 +616,7 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
     extern __shared__ int s_dyn[];
     const int E = p.E, G = gridDim.x, g = blockIdx.x, k = p.k;
     int* s_base = s_dyn;        // [E] sorted position of the CTA's next slot of the expert
-    int* s_delta = s_base + E;  // [E] tile row minus sorted position
-    int* s_row = s_delta + E;   // [32][E] a warp's counts, then its first positions
+    int* s_row = s_base + E;    // [32][E] a warp's counts, then its first positions
     __shared__ int s_sums[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t t0 = mp_token(p.T, g, G), t1 = mp_token(p.T, g + 1, G);
@@ -652,23 +669,19 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
                 before += s_row[i * 2 * Ep + tid];
                 all += s_row[(i * 2 + 1) * Ep + tid];
             }
-        int S, tiles, padded;
+        int S, tiles;
         const int b = cta_prefix(all, s_sums, &S);
         const int q = cta_prefix((all + kMxBN - 1) / kMxBN, s_sums, &tiles);
-        const int pad = cta_prefix((all + 7) & ~7, s_sums, &padded);
         if (tid < E) {
             s_base[tid] = b + before;
-            s_delta[tid] = pad - b;
             if (g == 0) {
                 p.bounds[tid] = b;
                 p.ntile_prefix[tid] = q;
-                p.pad_start[tid] = pad;
             }
         }
         if (g == 0 && tid == 0) {
             p.bounds[E] = S;
             p.ntile_prefix[E] = tiles;
-            p.pad_start[E] = padded;
             p.hdr[kHdrTiles] = tiles;
         }
     }
@@ -703,16 +716,16 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
         if (e >= 0) {
             const int pos = s_row[warp * E + e] + rank;
             p.ids_dst[pos] = i;
-            p.slot_prow[i] = pos + s_delta[e];
+            p.ids_src[pos] = p.per_slot ? i : i / k;
         }
         __syncthreads();
     }
     // round the CTA's rows, four planes of a row to a warp at a time
-    const int planes = (p.n_in + 255) / 256, chunks = (planes + kMxPlanes - 1) / kMxPlanes, copies = p.per_slot ? 1 : k;
+    const int planes = (p.n_in + 255) / 256, chunks = (planes + kMxPlanes - 1) / kMxPlanes;
     const int dr = 32 / chunks, dc = 32 % chunks;
     int64_t r = r0 + warp / chunks;
     for (int c = warp % chunks; r < r1; r += dr) {
-        round_planes<TYPE>(p.x, r, p.n_in, c * kMxPlanes, planes, p.slot_prow + r * copies, copies, p.rows, lane);
+        round_planes<TYPE>(p.x, r, p.n_in, c * kMxPlanes, planes, p.rows, lane);
         c += dc;
         if (c >= chunks) {
             c -= chunks;
@@ -1218,7 +1231,7 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
 template <int TYPE>
 moe_status launch_place(const MxPlaceArgs& a, unsigned grid, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    if (!allow_smem(mx4_place_kernel<TYPE>, (int)(34 * kRidMaxE * sizeof(int)), done)) return MOE_ERR_CUDA;
+    if (!allow_smem(mx4_place_kernel<TYPE>, (int)(33 * kRidMaxE * sizeof(int)), done)) return MOE_ERR_CUDA;
     return launch_dependent(mx4_place_kernel<TYPE>, grid, kMpThreads, smem, s, a);
 }
 
@@ -1296,15 +1309,13 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
         prof_mark(s, "decode");
         return st;
     }
-    // The rounded rows take the workspace of the 16-bit ones: 128 bytes per 256
-    // values and 4 per 128 where those take 128 per 64.  Only up to 64 values do
-    // the scales not fit behind the codes; there they take the rows' factors.
+    // the rounded rows take the place of the 16-bit ones (128 bytes per 64 values)
     MxRows o;
-    o.rows_pad = W.rows_pad;
-    o.scale_ld = (W.rows_pad + 3) / 4 * 4;  // bulk copies start on 16 bytes
+    o.pitch = p.L.kt_count * 32;
+    o.scale_pitch = planes * 8;
+    const int64_t rows = mode == MOE_BROADCAST ? n_tokens : S;
     o.codes = (uint8_t*)(ws + W.xt);
-    o.scales = n_in <= kTileK ? (uint32_t*)(ws + W.xs)
-                              : (uint32_t*)(o.codes + (size_t)planes * W.rows_pad * 128u);
+    o.scales = o.codes + rows * o.pitch;
     const bool broadcast = mode == MOE_BROADCAST;
     prof_begin(s);
     moe_status st;
@@ -1315,11 +1326,10 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
         prof_mark(s, "row_ids");
         MxPlaceArgs a = {ids, x, n_in, n_tokens, k, n_experts, !broadcast, counts, (int32_t*)(ws + W.bounds),
-                         (int32_t*)(ws + W.tiles), (int32_t*)(ws + W.pad), (int32_t*)(ws + W.dst),
-                         (int32_t*)(ws + W.sprow), hdr, o};
+                         (int32_t*)(ws + W.tiles), (int32_t*)(ws + W.src1), (int32_t*)(ws + W.dst), hdr, o};
         const int Ep = (n_experts + 31) & ~31;
-        const size_t rows = 32 * (size_t)n_experts, sums = 2 * (size_t)(kMpThreads / Ep) * Ep;
-        const size_t smem = (2 * (size_t)n_experts + (rows > sums ? rows : sums)) * sizeof(int);
+        const size_t ranks = 32 * (size_t)n_experts, sums = 2 * (size_t)(kMpThreads / Ep) * Ep;
+        const size_t smem = ((size_t)n_experts + (ranks > sums ? ranks : sums)) * sizeof(int);
         st = x_type == MOE_BF16  ? launch_place<MOE_BF16>(a, G, smem, s)
              : x_type == MOE_F16 ? launch_place<MOE_F16>(a, G, smem, s)
                                  : launch_place<MOE_F32>(a, G, smem, s);
@@ -1330,26 +1340,24 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
                             (int32_t*)(ws + W.pad), (int32_t*)(ws + W.sprow), kMxBN, hdr, nullptr, s, &n_rid);
         if (st) return st;
         prof_mark(s, "row_ids", n_rid);
-        const int64_t rows = broadcast ? n_tokens : S, blocks = (rows + 7) / 8, cap = (int64_t)mx_sm_count() * 8;
+        const int64_t blocks = (rows + 7) / 8, cap = (int64_t)mx_sm_count() * 8;
         const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
-        const int32_t* prow = (const int32_t*)(ws + W.sprow);
-        const int copies = broadcast ? k : 1;
-        if (x_type == MOE_BF16) mx4_gather_kernel<MOE_BF16><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
-        else if (x_type == MOE_F16) mx4_gather_kernel<MOE_F16><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
-        else mx4_gather_kernel<MOE_F32><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
+        if (x_type == MOE_BF16) mx4_round_kernel<MOE_BF16><<<grid, 256, 0, s>>>(x, n_in, rows, o, hdr);
+        else if (x_type == MOE_F16) mx4_round_kernel<MOE_F16><<<grid, 256, 0, s>>>(x, n_in, rows, o, hdr);
+        else mx4_round_kernel<MOE_F32><<<grid, 256, 0, s>>>(x, n_in, rows, o, hdr);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (st) return st;
-    prof_mark(s, "gather");
+    prof_mark(s, "round");
     p.tiles_per_unit = 2;
     p.n_groups = n_experts;
     p.bounds = (const int32_t*)(ws + W.bounds);
     p.ntile_prefix = (const int32_t*)(ws + W.tiles);
-    p.pad_start = (const int32_t*)(ws + W.pad);
     p.B = o.codes;
     p.BS = o.scales;
-    p.rows_pad = o.rows_pad;
-    p.scale_ld = o.scale_ld;
+    p.b_pitch = o.pitch;
+    p.bs_pitch = o.scale_pitch;
+    p.src_rows = (const int32_t*)(ws + W.src1);
     p.dst_rows = (const int32_t*)(ws + W.dst);
     st = launch_mx4_gemm(p, (S + kMxBN - 1) / kMxBN + (S < n_experts ? S : n_experts), s);
     prof_mark(s, "gemm");
