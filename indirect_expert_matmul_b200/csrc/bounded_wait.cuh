@@ -31,14 +31,16 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
     }
 }
 
-// lane 0 waits, the warp learns the outcome
+// lane 0 waits, the warp learns the outcome (CLUSTER: of arrivals by another CTA too)
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
                                           long long limit) {
     // every lane polls (no lane-0 branch); lanes that see different phases simply poll again
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (!CLUSTER && ptx::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
-        if (ptx::mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
+        if (CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait_sleep(bar, parity, kSleepNs))
+            return true;
         if (*abort_flag) return false;
         if (clock64() - t0 > limit) {
             if ((threadIdx.x & 31) == 0) {

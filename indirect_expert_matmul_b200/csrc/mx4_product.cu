@@ -2,12 +2,19 @@
 //   dst[t][s] = W[ids[t][s]] . Q(x[t] or x[t][s]),
 // Q rounding every 32 consecutive values to one E8M0 scale and E2M1 codes.
 //
-// Rounding: each source row is rounded once to a row of codes (two to a byte, K
-// order) and a row of scale words (four scale bytes for 128 values).
+// Quantising gather: each row is rounded once and its codes go to the tile rows
+// of every slot that reads it: [K plane of 256 values][row][128 bytes], 16-byte
+// chunk c at c ^ (row % 8) (the 128-byte swizzle); the scales of 128 values of
+// a row are one word of [K / 128][row].
 //
-// Grouped GEMM (tcgen05 kind::mxf4, block scales): a CTA takes units of (up to
-// 192 sorted rows of one expert) x (one or two 128-row weight tiles) and streams
-// K in stages of 256 values.  The 4-bit weights go from their repacked form
+// Grouped GEMM (tcgen05 kind::mxf4, block scales): a pair of CTAs takes units of
+// (up to 192 sorted rows of one expert) x (two 128-row weight tiles, one a CTA)
+// and streams K in stages of 256 values; a pair MMA reads both CTAs' tiles and
+// half of the rows from each, so that every SM fetches a tile and half the rows
+// for 128 x 192 results - the L2 bytes of a 256 x 192 unit of one CTA - and
+// tensor memory has room for two accumulators: one is drained while the next
+// fills (one CTA a unit had to stop for the drain, 6000 of 20000 cycles a unit
+// of the skewed 8192-token product).  The 4-bit weights go from their repacked form
 // straight to the tensor cores, no thread touches them.  The codes of a 32-row
 // sub-block are 32 rows of 32 bytes, which the MMA reads in the 32-byte swizzle
 // (address bit 4 ^= bit 7).  Copied as such, in boxes 32 bytes wide, they kept
@@ -39,26 +46,24 @@ bool testing_stall_state(int* cta, int* stage, long long* limit_cycles);
 namespace {
 
 // ----------------------------------------------------------------- geometry
-constexpr int kMxThreads = 640;
-constexpr int kMxGather = 128;    // threads that gather the rows' codes and scales
+constexpr int kMxThreads = 512;
 constexpr int kMxBN = kGemmBN;    // sorted rows (columns of the accumulator) of a unit
 constexpr int kMxStageKt = 4;     // 64-value k-steps of a stage
-constexpr int kMxStages = 3;
+constexpr int kMxStages = 7;
+constexpr int kMxScaleSlots = 5;  // stages whose scales have a place in tensor memory
 constexpr uint32_t kMxCodes = kTileM * 32;                 // codes of a tile's k-step
 constexpr uint32_t kMxACodes = kMxStageKt * kMxCodes;      // 16384
 constexpr uint32_t kMxAScales = kMxStageKt * kTileM * 2;   // 1024
-constexpr uint32_t kMxB = kMxBN * 128;                     // 24576
-constexpr uint32_t kMxBScales = kMxBN * 8;                 // 1536: a row's two words
-constexpr uint32_t kMxStageBytes = 2 * kMxACodes + kMxB + 2 * kMxAScales + kMxBScales;
-static_assert(kMxStageBytes % 1024 == 512, "stages are padded to the swizzle's 1024 bytes below");
-constexpr uint32_t kMxStagePitch = (kMxStageBytes + 1023) / 1024 * 1024;
-constexpr uint32_t kMxOffB = 2 * kMxACodes, kMxOffAS = kMxOffB + kMxB, kMxOffBS = kMxOffAS + 2 * kMxAScales;
+constexpr uint32_t kMxB = kMxBN / 2 * 128;                 // 12288: half the rows
+constexpr uint32_t kMxBScales = 2 * kMxBN * 4;             // 1536: every row's two words
+constexpr uint32_t kMxOffB = kMxACodes, kMxOffAS = kMxOffB + kMxB, kMxOffBS = kMxOffAS + kMxAScales;
+constexpr uint32_t kMxStagePitch = (kMxOffBS + kMxBScales + 1023) / 1024 * 1024;
 constexpr uint32_t kMxBarOff = kMxStages * kMxStagePitch;
 constexpr uint32_t kMxSmem = kMxBarOff + 256 + 1024;
-// tensor memory: two accumulators, then per stage 16 columns of A scales
-// (two tiles x two 128-value halves x four) and 16 of B scales (two halves x eight)
-constexpr uint32_t kMxScaleCol0 = 2 * kMxBN;
-static_assert(kMxScaleCol0 + kMxStages * 32 <= 512, "accumulators and scales fill tensor memory");
+// tensor memory: two accumulators, then per slot 8 columns of A scales (two
+// 128-value halves x four) and 16 of B scales (two halves x eight)
+constexpr uint32_t kMxScaleCol0 = 2 * kMxBN, kMxScaleCols = 24;
+static_assert(kMxScaleCol0 + kMxScaleSlots * kMxScaleCols <= 512, "accumulators and scales fill tensor memory");
 constexpr int kMxSmemGroups = 256;
 
 struct Mx4Params {
@@ -68,13 +73,12 @@ struct Mx4Params {
     WLayout L;
     int full_tiles;                 // tiles of 128 rows
     int tail_subs, tail_r;          // last tile: number of 32-row sub-blocks, of 16-row ones (0 or 1)
-    int tiles_per_unit;             // 1 or 2
     int n_groups;
-    const int32_t *bounds, *ntile_prefix;
-    const uint8_t* B;               // rounded source rows: codes, b_pitch bytes a row
-    const uint8_t* BS;              // and scales, bs_pitch bytes a row
-    int b_pitch, bs_pitch;
-    const int32_t *src_rows, *dst_rows;  // source row and row of dst of a sorted position
+    const int32_t *bounds, *ntile_prefix, *pad_start;
+    const uint8_t* B;               // codes [plane][rows_pad][128]
+    const uint32_t* BS;             // scales [K / 128][scale_ld]
+    int64_t rows_pad, scale_ld;
+    const int32_t* dst_rows;
     float* out;
     int out_ld;
     int* hdr;
@@ -131,14 +135,17 @@ __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xf
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 struct MxTile {
-    int e, mu, p0, n;
+    int e, mu, p0, n, p0pad;
 };
+constexpr int kMxUnits = 4;  // units known ahead
 
-__global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
     extern __shared__ uint8_t smem_dyn[];
     __shared__ int s_prefix[kMxSmemGroups + 1];
     __shared__ int s_bounds[kMxSmemGroups + 1];
-    __shared__ __align__(16) int s_rows[8][kMxBN];
+    __shared__ int s_pad[kMxSmemGroups + 1];
+    __shared__ __align__(16) int s_rows[8][kMxBN / 2];
+    __shared__ MxTile s_unit[kMxUnits];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total;
 
@@ -146,35 +153,48 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
     uint64_t* full = (uint64_t*)(smem + kMxBarOff);  // a stage's copies have landed
     uint64_t* sf_full = full + kMxStages;            // its scales are in tensor memory
     uint64_t* empty = sf_full + kMxStages;           // its MMAs have completed
-    uint64_t* acc_full = empty + kMxStages;
-    uint64_t* acc_empty = acc_full + 1;
-    uint64_t* drained = acc_empty + 1;
+    uint64_t* acc_full = empty + kMxStages;          // [2]
+    uint64_t* acc_empty = acc_full + 2;              // [2]
+    uint64_t* unit_full = acc_empty + 2;             // [kMxUnits]
+    uint64_t* unit_empty = unit_full + kMxUnits;     // [kMxUnits]
+    uint64_t* drained = unit_empty + kMxUnits;
     volatile int* abort_flag = &s_abort;
     int* status = p.hdr + kHdrStatus;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = ptx::cluster_rank();  // of the pair; CTA 0 issues the MMAs
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const WLayout L = p.L;
-    const int MT = L.mt_count, KT = L.kt_count, KS = (KT + kMxStageKt - 1) / kMxStageKt;
-    const int TPU = p.tiles_per_unit, MU = (MT + TPU - 1) / TPU;
+    const int MT = L.mt_count, KT = L.kt_count, KS = (KT + kMxStageKt - 1) / kMxStageKt, MU = (MT + 1) / 2;
     const bool in_smem = p.n_groups <= kMxSmemGroups;
 
     if (tid == 0) {
         for (int i = 0; i < kMxStages; ++i) {
-            ptx::mbar_init(&full[i], 2 + kMxGather);
-            ptx::mbar_init(&sf_full[i], 4);
+            ptx::mbar_init(&full[i], 2);
+            ptx::mbar_init(&sf_full[i], 8);
             ptx::mbar_init(&empty[i], 1);
         }
-        ptx::mbar_init(acc_full, 1);
-        ptx::mbar_init(acc_empty, 8);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&acc_full[i], 1);
+            ptx::mbar_init(&acc_empty[i], 16);
+        }
+        for (int i = 0; i < kMxUnits; ++i) {
+            ptx::mbar_init(&unit_full[i], 1);
+            ptx::mbar_init(&unit_empty[i], rank == 0 ? 11 : 10);  // two copy warps, eight that drain, the MMAs'
+        }
         ptx::mbar_init(drained, 1);
         s_abort = 0;
         ptx::fence_mbar_init();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(&s_tmem, 512);
-        ptx::tmem_relinquish();
+        ptx::tmem_alloc_pair(&s_tmem, 512);
+        ptx::tmem_relinquish_pair();
     }
-    // (a programmatic dependent of the gather: nothing it wrote is read before it has ended)
+    ptx::tc_fence_before();
+    ptx::cluster_sync();  // both CTAs' barriers are set up
+    ptx::tc_fence_after();
+    const uint32_t tmem = uniform(s_tmem);
+    // (a programmatic dependent of the rounding: nothing it wrote is read before it has ended)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // (all threads by one thread's reading: another CTA may set the status meanwhile)
     if (tid == 0) s_total = read_status(status) != 0 ? 0 : p.hdr[kHdrTiles] * MU;
@@ -184,51 +204,61 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         for (int i = tid; i <= p.n_groups; i += kMxThreads) {
             s_prefix[i] = p.ntile_prefix[i];
             s_bounds[i] = p.bounds[i];
+            s_pad[i] = p.pad_start[i];
         }
-    ptx::tc_fence_before();
     __syncthreads();
-    ptx::tc_fence_after();
-    const uint32_t tmem = uniform(s_tmem);
 
+    // Unit t, by a whole warp: the largest group whose first column tile is at most
+    // q, 32 candidates a step (by bisection a unit's start cost ~1000 cycles).
     auto unit = [&](int t) {
         MxTile r;
         const int q = t / MU;
         r.mu = t - q * MU;
-        const int* pre = in_smem ? s_prefix : p.ntile_prefix;
-        const int* bnd = in_smem ? s_bounds : p.bounds;
         int lo = 0, hi = p.n_groups;  // pre[lo] <= q < pre[hi]
         while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= q) lo = mid; else hi = mid;
+            const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+            const bool below = at < hi && (in_smem ? s_prefix[at] : __ldg(p.ntile_prefix + at)) <= q;
+            lo += (__popc(__ballot_sync(0xffffffffu, below)) - 1) * step;
+            hi = min(hi, lo + step);
         }
         r.e = lo;
-        const int j = q - pre[lo];
-        r.p0 = bnd[lo] + j * kMxBN;
-        r.n = min(kMxBN, bnd[lo + 1] - r.p0);
+        const int j = q - (in_smem ? s_prefix[lo] : __ldg(p.ntile_prefix + lo));
+        const int first = in_smem ? s_bounds[lo] : __ldg(p.bounds + lo);
+        r.p0 = first + j * kMxBN;
+        r.p0pad = (in_smem ? s_pad[lo] : __ldg(p.pad_start + lo)) + j * kMxBN;
+        r.n = min(kMxBN, (in_smem ? s_bounds[lo + 1] : __ldg(p.bounds + lo + 1)) - r.p0);
         return r;
     };
 
-    if (warp == 0 || warp == 2) {
+    // Units are found by warp 3, up to kMxUnits ahead; the others take them from
+    // shared memory (found by each role itself, a unit's start was a gap of 2500
+    // cycles in the MMAs).
+    auto take_unit = [&](int k, MxTile& u) {
+        const int slot = k % kMxUnits;
+        if (!warp_wait(&unit_full[slot], (uint32_t)(k / kMxUnits) & 1u, abort_flag, status, p.wait_limit)) return false;
+        u = s_unit[slot];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&unit_empty[slot]);
+        return true;
+    };
+
+    if (warp == 0) {
         // ------------------------------------------------------------ weights
-        // The codes and scales of the unit's first (warp 0) and second weight tile.
-        // One thread issuing all of a stage's copies needed ~1300 cycles for it, twice
-        // the MMAs' time.
         const uint32_t issue = ptx::elect_one();
-        const int i = warp >> 1;
         int s = 0;
         uint32_t ph = 0, used = 0, par = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const MxTile u = unit(t);
-            const int mt = u.mu * TPU + i;
+        for (int t = pair, k = 0; t < total && ok; t += pairs, ++k) {
+            MxTile u;
+            ok = take_unit(k, u);
+            if (!ok) break;
+            const int mt = u.mu * 2 + (int)rank;
             for (int ks = 0; ks < KS; ++ks) {
                 ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 uint8_t* st = smem + s * kMxStagePitch;
                 if (issue) {
-                    if (i < TPU && mt < MT)
-                        load_weights<kMxStageKt>(p, L, st + i * kMxACodes, st + kMxOffAS + i * kMxAScales, u.e, mt, ks,
-                                                 &full[s]);
+                    if (mt < MT) load_weights<kMxStageKt>(p, L, st, st + kMxOffAS, u.e, mt, ks, &full[s]);
                     else ptx::mbar_arrive(&full[s]);
                 }
                 used |= 1u << s;
@@ -241,90 +271,81 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
         volatile int never = 0;
         for (int j = 0; j < kMxStages; ++j)
             if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, p.wait_limit);
-    } else if (warp >= 16) {
+    } else if (warp == 2) {
         // --------------------------------------------------------------- rows
-        // The unit's rows lie anywhere in the rounded source rows (a token's row serves
-        // k experts): eight lanes copy the 128 bytes of a row's stage, four rows an
-        // instruction, into the 128-byte swizzle the MMA reads.  (Copying every row to
-        // a place in its expert's order first cost 117 MB written and read again in
-        // the 4096-token gate product.)  The copies are generic-proxy writes: the scale
-        // warps fence them for the MMAs.
-        const int g = warp - 16, c = lane & 7;
-        const uint32_t smem_a = ptx::smem_u32(smem);
+        // This CTA's half of the unit's rows (contiguous and swizzled) and every
+        // row's scales.
+        const uint32_t issue = ptx::elect_one();
         int s = 0, q = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const MxTile u = unit(t);
-            const uint8_t* src[kMxBN / 16];  // of rows 16 i + 4 g + lane / 8
-            const uint8_t* ssrc[2];          // of rows 48 g + lane, 48 g + 32 + lane
-#pragma unroll
-            for (int i = 0; i < kMxBN / 16; ++i) {
-                const int r = 16 * i + 4 * g + (lane >> 3);
-                src[i] = p.B + (r < u.n ? (int64_t)__ldg(p.src_rows + u.p0 + r) * p.b_pitch + c * 16 : 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 48 * g + 32 * i + lane;
-                ssrc[i] = p.BS + (r < u.n && (i == 0 || lane < 16)
-                                      ? (int64_t)__ldg(p.src_rows + u.p0 + r) * p.bs_pitch : 0);
-            }
+        for (int t = pair, k = 0; t < total && ok; t += pairs, ++k) {
+            MxTile u;
+            ok = take_unit(k, u);
+            if (!ok) break;
+            const uint32_t nh = (uint32_t)(u.n + 31) / 32u * 16u;
+            const uint8_t* bsrc = p.B + (size_t)(u.p0pad + (int)(rank * nh)) * 128u;
+            const uint32_t* ssrc = p.BS + u.p0pad;
             for (int ks = 0; ks < KS; ++ks, ++q) {
                 ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
                 if (!ok) break;
-                if (!((int)blockIdx.x == p.stall_cta && q == p.stall_stage)) {
-                    const uint32_t st = smem_a + s * kMxStagePitch;
-                    const bool in_k = ks * 128 + c * 16 < p.b_pitch;
-#pragma unroll
-                    for (int i = 0; i < kMxBN / 16; ++i) {
-                        const int r = 16 * i + 4 * g + (lane >> 3);
-                        if (r < u.n && in_k)
-                            ptx::cp_async16(st + kMxOffB + r * 128 + ((c ^ (r & 7)) << 4), src[i] + ks * 128);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = 48 * g + 32 * i + lane;
-                        if (r < u.n && (i == 0 || lane < 16))
-                            ptx::cp_async8(st + kMxOffBS + r * 8, ssrc[i] + ks * 8);
-                    }
-                    ptx::cp_async_arrive(&full[s]);
+                if (issue && !((int)blockIdx.x == p.stall_cta && q == p.stall_stage)) {
+                    uint8_t* st = smem + s * kMxStagePitch;
+                    const bool two = KT - ks * kMxStageKt > 2;  // the stage's second 128 values
+                    ptx::mbar_arrive_expect_tx(&full[s], nh * 128u + (two ? nh * 16u : nh * 8u));
+                    ptx::bulk_g2s(st + kMxOffB, bsrc, nh * 128u, &full[s]);
+                    ptx::bulk_g2s(st + kMxOffBS, ssrc, nh * 8u, &full[s]);
+                    if (two) ptx::bulk_g2s(st + kMxOffBS + kMxBN * 4, ssrc + p.scale_ld, nh * 8u, &full[s]);
                 }
+                __syncwarp();
+                bsrc += (size_t)p.rows_pad * 128u;
+                ssrc += 2 * p.scale_ld;
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
         }
-        ptx::cp_async_wait_all();
-    } else if (warp == 1) {
+    } else if (warp == 3) {
+        // -------------------------------------------------------------- units
+        bool ok = true;
+        for (int t = pair, k = 0; t < total && ok; t += pairs, ++k) {
+            const int slot = k % kMxUnits;
+            const MxTile u = unit(t);
+            ok = warp_wait(&unit_empty[slot], ((uint32_t)(k / kMxUnits) & 1u) ^ 1u, abort_flag, status, p.wait_limit);
+            if (!ok) break;
+            if (lane == 0) {
+                s_unit[slot] = u;
+                ptx::mbar_arrive(&unit_full[slot]);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 1 && rank == 0) {
         // -------------------------------------------------------------- MMAs
         const uint32_t issue = ptx::elect_one(), smem_a = ptx::smem_u32(smem);
-        int s = 0;
+        int s = 0, slot = 0;
         uint32_t ph = 0, use = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const MxTile u = unit(t);
-            const int n16 = (u.n + 15) & ~15;
-            const uint32_t id0 = ptx::idesc_mxf4(n16, 0), id1 = ptx::idesc_mxf4(n16, 1);
-            const bool two = TPU == 2 && u.mu * 2 + 1 < MT;
-            ok = warp_wait(acc_empty, (use & 1) ^ 1, abort_flag, status, p.wait_limit);
+        for (int t = pair; t < total && ok; t += pairs, ++use) {
+            MxTile u;
+            ok = take_unit((int)use, u);
             if (!ok) break;
-            use += 1;
+            const int n32 = (u.n + 31) & ~31;
+            const uint32_t id0 = ptx::idesc_mxf4(n32, 0, 256), id1 = ptx::idesc_mxf4(n32, 1, 256), buf = use & 1;
+            const uint32_t d = tmem + buf * kMxBN;
+            ok = warp_wait<true>(&acc_empty[buf], ((use >> 1) & 1) ^ 1, abort_flag, status, p.wait_limit);
+            if (!ok) break;
             for (int ks = 0; ks < KS; ++ks) {
-                // (the scale warps arrive after they have seen the stage's copies land)
-                ok = warp_wait(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+                // (the scale warps of both CTAs arrive after they have seen the stage's copies land)
+                ok = warp_wait<true>(&sf_full[s], ph, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint32_t st = smem_a + (uint32_t)s * kMxStagePitch;
-                const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)s * 32u;
+                const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)slot * kMxScaleCols;
                 const uint64_t ad = ptx::desc_k_sw32(st), bd = ptx::desc_k_sw128(st + kMxOffB);
                 const int kts = KT - ks * kMxStageKt;
                 if (issue) {
                     // one branch for all of a stage's MMAs: a predicate on each cost ~80 cycles an MMA
                     auto step = [&](int j) {  // address fields count 16 bytes; sums stay inside their 14 bits
-                        const uint32_t id = j & 1 ? id1 : id0;
-                        ptx::mma_mxf4_ss(tmem, ad + (j * kMxCodes >> 4), bd + j * 2, id, sf + (j >> 1) * 4,
-                                         sf + 16 + (j >> 1) * 8, (ks | j) != 0);
-                        if (two)
-                            ptx::mma_mxf4_ss(tmem + kMxBN, ad + ((kMxACodes + j * kMxCodes) >> 4), bd + j * 2, id,
-                                             sf + 8 + (j >> 1) * 4, sf + 16 + (j >> 1) * 8, (ks | j) != 0);
+                        ptx::mma_mxf4_pair(d, ad + (j * kMxCodes >> 4), bd + j * 2, j & 1 ? id1 : id0, sf + (j >> 1) * 4,
+                                           sf + 8 + (j >> 1) * 8, (ks | j) != 0);
                     };
                     if (kts >= kMxStageKt) {
 #pragma unroll
@@ -332,18 +353,19 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
                     } else {
                         for (int j = 0; j < kts; ++j) step(j);
                     }
-                    ptx::mma_commit(&empty[s]);
+                    ptx::mma_commit_pair(&empty[s]);
                 }
                 __syncwarp();
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
+                if (++slot == kMxScaleSlots) slot = 0;
             }
             if (!ok) break;
-            if (issue) ptx::mma_commit(acc_full);
+            if (issue) ptx::mma_commit_pair(&acc_full[buf]);
             __syncwarp();
         }
-        // every MMA issued has completed before the CTA can release tensor memory
+        // every MMA issued has completed before the CTAs can release tensor memory
         if (issue) {
-            ptx::mma_commit(drained);
+            ptx::mma_commit_pair(drained);
             volatile int never = 0;
             wait_bar(drained, 0, &never, status, p.wait_limit);
         }
@@ -351,102 +373,109 @@ __global__ void __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_co
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------- scales, per stage
         // Every warp writes its quarter of the lanes with the same words: lane r
-        // holds rows r, 32 + r, ... of a tile (or of the sorted rows), one column each.
-        int s = 0;
-        uint32_t ph = 0;
+        // holds rows r, 32 + r, ... of the tile (or of the sorted rows), one column each.
+        int s = 0, slot = 0;
+        int old = -kMxScaleSlots;  // the stage that had the slot before, counted on (negative: none)
+        uint32_t ph = 0, old_ph = 0;
         bool ok = true;
         const uint32_t dst = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + kMxScaleCol0;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int t = pair; t < total && ok; t += pairs) {
             for (int ks = 0; ks < KS; ++ks) {
-                ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit);
+                ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
+                     (old < 0 || warp_wait(&empty[old], old_ph, abort_flag, status, p.wait_limit));
                 if (!ok) break;
+                if (++old == kMxStages) { old = 0; old_ph ^= 1; }
                 const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS);
-                const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 8;
-                ptx::fence_proxy_async_smem();  // the gathered rows, for the MMAs
-                uint32_t v[32];
+                const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 4;
+                uint32_t v[8], w[16];
                 weight_scales(as, lane, v);
-                weight_scales(as + kMxAScales, lane, v + 8);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint2 w = c < kMxBN / 32 ? ptx::lds64(bs + c * 256) : make_uint2(0u, 0u);
-                    v[16 + c] = w.x;
-                    v[24 + c] = w.y;
-                }
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        w[h * 8 + c] = c < kMxBN / 32 ? ptx::lds32(bs + h * (kMxBN * 4) + c * 128) : 0u;
                 ptx::tc_fence_after();
-                ptx::tmem_st_32x32b_x32(dst + (uint32_t)s * 32u, v);
+                ptx::tmem_st_32x32b_x8(dst + (uint32_t)slot * kMxScaleCols, v);
+                ptx::tmem_st_32x32b_x16(dst + (uint32_t)slot * kMxScaleCols + 8u, w);
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&sf_full[s]);
+                if (lane == 0) ptx::mbar_arrive_cluster<false>(&sf_full[s], 0);
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
+                if (++slot == kMxScaleSlots) slot = 0;
             }
         }
     } else if (warp >= 8 && warp < 16) {
         // ---------------------------------------------------------- epilogue
-        // Warps 8-11 drain the first tile's accumulator, 12-15 the second's.
-        const int wq = warp & 3, i = (warp - 8) >> 2;
-        int* rows = s_rows[warp - 8];  // the warp's copy of the unit's output rows
+        // Four warps (a lane quarter each) drain the first 96 columns, four the rest.
+        const int wq = warp & 3, half = (warp - 8) >> 2;
+        int* rows = s_rows[warp - 8];  // the output rows of the warp's columns
         uint32_t use = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
-            const MxTile u = unit(t);
-            const int mt = u.mu * TPU + i;
-            const bool live = i < TPU && mt < MT;
+        for (int t = pair; t < total; t += pairs, ++use) {
+            MxTile u;
+            if (!take_unit((int)use, u)) break;
+            const int mt = u.mu * 2 + (int)rank, c_lo = half * (kMxBN / 2), n = min(kMxBN / 2, u.n - c_lo);
+            const uint32_t buf = use & 1;
             __syncwarp();
-            for (int c = lane; c < u.n; c += 32) rows[c] = __ldg(p.dst_rows + u.p0 + c);
+            for (int c = lane; c < n; c += 32) rows[c] = __ldg(p.dst_rows + u.p0 + c_lo + c);
             __syncwarp();
-            if (!warp_wait(acc_full, use & 1, abort_flag, status, p.wait_limit)) break;
-            use += 1;
+            if (!warp_wait(&acc_full[buf], (use >> 1) & 1, abort_flag, status, p.wait_limit)) break;
             ptx::tc_fence_after();
-            if (live) {
-                const int m = mt * kTileM + 32 * wq + perm_row(lane);
-                const bool m_ok = m < L.n_out;
-                float* out = p.out + m;
-                // A column is a sorted row: its 32 lanes are 128 consecutive bytes of one
-                // row of dst.  The rows' numbers come from shared memory, four to a load: by
-                // shuffles under a test a column cost 105 cycles (20000 a unit) against ~25.
-                for (int c0 = 0; c0 < u.n; c0 += 32) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + i * kMxBN + c0, v);
-                    ptx::tmem_ld_wait();
-                    if (!m_ok) continue;
-                    if (c0 + 32 <= u.n) {
+            const int m = mt * kTileM + 32 * wq + perm_row(lane);
+            const bool m_ok = mt < MT && m < L.n_out;
+            float* out = p.out + m;
+            // A column is a sorted row: its 32 lanes are 128 consecutive bytes of one
+            // row of dst.  The rows' numbers come from shared memory, four to a load: by
+            // shuffles under a test a column cost 105 cycles against ~25.
+            for (int c0 = 0; c0 < n; c0 += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + buf * kMxBN + c_lo + c0, v);
+                ptx::tmem_ld_wait();
+                if (!m_ok) continue;
+                if (c0 + 32 <= n) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const int4 r = *(const int4*)(rows + c0 + j);
-                            out[(int64_t)r.x * p.out_ld] = __uint_as_float(v[j]);
-                            out[(int64_t)r.y * p.out_ld] = __uint_as_float(v[j + 1]);
-                            out[(int64_t)r.z * p.out_ld] = __uint_as_float(v[j + 2]);
-                            out[(int64_t)r.w * p.out_ld] = __uint_as_float(v[j + 3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c0 + j < u.n) out[(int64_t)rows[c0 + j] * p.out_ld] = __uint_as_float(v[j]);
+                    for (int j = 0; j < 32; j += 4) {
+                        const int4 r = *(const int4*)(rows + c0 + j);
+                        out[(int64_t)r.x * p.out_ld] = __uint_as_float(v[j]);
+                        out[(int64_t)r.y * p.out_ld] = __uint_as_float(v[j + 1]);
+                        out[(int64_t)r.z * p.out_ld] = __uint_as_float(v[j + 2]);
+                        out[(int64_t)r.w * p.out_ld] = __uint_as_float(v[j + 3]);
                     }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < n) out[(int64_t)rows[c0 + j] * p.out_ld] = __uint_as_float(v[j]);
                 }
-                __syncwarp();
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(acc_empty);
+            if (lane == 0) ptx::mbar_arrive_cluster<false>(&acc_empty[buf], 0);
         }
     }
 
+    // (the other CTA's MMAs read this one's memory, its warps arrive on this one's barriers)
     ptx::tc_fence_before();
     __syncthreads();
+    if (warp == 1 && rank == 1) {  // the last arrival of the pair's MMAs on this CTA
+        volatile int never = 0;
+        warp_wait<true>(drained, 0, &never, status, p.wait_limit);
+    }
+    __syncwarp();
+    ptx::cluster_sync();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc_pair(tmem, 512);
     }
 }
 
 // -------------------------------------------------------- quantising gather
-// Where the rounded rows go, in the order of the source rows: 32 code bytes a
-// 64-value k-step (padded with zeros), and two scale words a 256-value plane.
+// Where the rounded rows go: codes [plane of 256 values][row][128 bytes], the
+// 16-byte chunk of block c at c ^ (row % 8); scales [128 values][row], a word
+// of four scale bytes.
 struct MxRows {
     uint8_t* codes;
-    uint8_t* scales;
-    int pitch, scale_pitch;
+    uint32_t* scales;
+    int64_t rows_pad, scale_ld;
 };
 
 // Eight consecutive values as they lie in memory: maximum and codes.
@@ -505,10 +534,10 @@ struct MxEight {
 constexpr int kMxPlanes = 4;  // planes of a row a warp has in flight
 
 // Planes kp0 .. kp0 + 3 (256 values each) of source row r by one warp, eight
-// values a lane, four lanes a block.
+// values a lane, four lanes a block, to the tile rows prow[0 .. copies).
 template <int TYPE>
 __device__ __forceinline__ void round_planes(const void* __restrict__ x, int64_t r, int n_in, int kp0, int planes,
-                                             const MxRows& o, int lane) {
+                                             const int32_t* prow, int copies, const MxRows& o, int lane) {
     constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
     const int col = kp0 * 256 + lane * 8;
     const char* src = (const char*)x + (r * n_in + col) * esz;
@@ -518,37 +547,49 @@ __device__ __forceinline__ void round_planes(const void* __restrict__ x, int64_t
         if (col + i * 256 < n_in) v[i].load(src + i * 256 * esz);
         else v[i].zero();
     }
-    uint8_t* codes = o.codes + r * o.pitch + kp0 * 128 + lane * 4;
-    const int left = o.pitch - kp0 * 128 - lane * 4;
-    uint32_t word = 0u;  // lanes 0-7: the scale word of half lane % 2 of plane lane / 2
+    uint32_t w[kMxPlanes], sw[kMxPlanes];
 #pragma unroll
     for (int i = 0; i < kMxPlanes; ++i) {
         uint32_t m = v[i].amax_bits();
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const uint32_t X = mx_scale_byte(m);
-        const uint32_t w = X == 255u ? 0u : v[i].codes(mx_inv_scale(X));
-        if (i * 128 < left) *(uint32_t*)(codes + i * 128) = w;
-        uint32_t sw = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
-        sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
-        sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
-        const uint32_t half = __shfl_sync(0xffffffffu, sw, (lane & 1) * 16);
-        if ((lane >> 1) == i) word = half;
+        w[i] = X == 255u ? 0u : v[i].codes(mx_inv_scale(X));
+        sw[i] = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
+        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 4);
+        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 8);
     }
-    if (lane < 2 * kMxPlanes && kp0 + (lane >> 1) < planes)
-        *(uint32_t*)(o.scales + r * o.scale_pitch + kp0 * 8 + lane * 4) = word;
+    const size_t pitch = (size_t)o.rows_pad * 128u;
+    uint8_t* plane = o.codes + (size_t)kp0 * pitch + (lane & 3) * 4;
+    uint32_t* sp = o.scales + (size_t)(2 * kp0 + (lane >> 4)) * o.scale_ld;
+    const bool sc = (lane & 15) == 0;
+    for (int j = 0; j < copies; ++j) {
+        const uint32_t pr = (uint32_t)prow[j];
+        uint8_t* c = plane + ((size_t)pr * 128u + (((uint32_t)(lane >> 2) ^ (pr & 7u)) << 4));
+        uint32_t* q = sp + pr;
+#pragma unroll
+        for (int i = 0; i < kMxPlanes; ++i) {
+            if (kp0 + i < planes) *(uint32_t*)c = w[i];
+            if (sc && col + i * 256 < n_in) *q = sw[i];
+            c += pitch;
+            q += 2 * o.scale_ld;
+        }
+    }
 }
 
-// After the general row-id pass: one warp per source row.
+// After the general row-id pass: one warp per source row (broadcast: a token,
+// whose codes go to the tile rows of its k slots; per slot: one slot).
 template <int TYPE>
 __global__ void __launch_bounds__(256)
-mx4_round_kernel(const void* __restrict__ x, int n_in, int64_t n_rows, MxRows o, const int* hdr) {
+mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restrict__ slot_prow, int copies,
+                  int64_t n_rows, MxRows o, const int* hdr) {
     if (read_status(hdr + kHdrStatus) != 0) return;
     const int lane = threadIdx.x & 31;
     const int planes = (n_in + 255) / 256;
     const int64_t nw = (int64_t)gridDim.x * (blockDim.x / 32);
     for (int64_t r = (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < n_rows; r += nw)
-        for (int kp = 0; kp < planes; kp += kMxPlanes) round_planes<TYPE>(x, r, n_in, kp, planes, o, lane);
+        for (int kp = 0; kp < planes; kp += kMxPlanes)
+            round_planes<TYPE>(x, r, n_in, kp, planes, slot_prow + r * copies, copies, o, lane);
 }
 
 // ------------------------------------------- row ids and gather in two launches
@@ -557,7 +598,7 @@ mx4_round_kernel(const void* __restrict__ x, int n_in, int64_t n_rows, MxRows o,
 // of the skewed 8192-token one): G CTAs count their tokens' slots by expert;
 // then each CTA sums the counts before its own (the place of its first slot of
 // every expert, the tables' prefixes), ranks its slots in slot order - the same
-// stable counting sort - and rounds its rows.
+// stable counting sort - and rounds its rows straight into their tile rows.
 // The second launch starts while the first runs and fetches its rows into L2.
 constexpr int kMpThreads = 1024;
 constexpr int64_t kMpPrefetch = 512 * 1024;
@@ -588,7 +629,7 @@ struct MxPlaceArgs {
     int64_t T;
     int k, E, per_slot;
     const int32_t* counts;
-    int32_t *bounds, *ntile_prefix, *ids_src, *ids_dst;
+    int32_t *bounds, *ntile_prefix, *pad_start, *ids_dst, *slot_prow;
     int* hdr;
     MxRows rows;
 };
@@ -616,7 +657,8 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
     extern __shared__ int s_dyn[];
     const int E = p.E, G = gridDim.x, g = blockIdx.x, k = p.k;
     int* s_base = s_dyn;        // [E] sorted position of the CTA's next slot of the expert
-    int* s_row = s_base + E;    // [32][E] a warp's counts, then its first positions
+    int* s_delta = s_base + E;  // [E] tile row minus sorted position
+    int* s_row = s_delta + E;   // [32][E] a warp's counts, then its first positions
     __shared__ int s_sums[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t t0 = mp_token(p.T, g, G), t1 = mp_token(p.T, g + 1, G);
@@ -669,19 +711,23 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
                 before += s_row[i * 2 * Ep + tid];
                 all += s_row[(i * 2 + 1) * Ep + tid];
             }
-        int S, tiles;
+        int S, tiles, padded;
         const int b = cta_prefix(all, s_sums, &S);
         const int q = cta_prefix((all + kMxBN - 1) / kMxBN, s_sums, &tiles);
+        const int pad = cta_prefix((all + 7) & ~7, s_sums, &padded);
         if (tid < E) {
             s_base[tid] = b + before;
+            s_delta[tid] = pad - b;
             if (g == 0) {
                 p.bounds[tid] = b;
                 p.ntile_prefix[tid] = q;
+                p.pad_start[tid] = pad;
             }
         }
         if (g == 0 && tid == 0) {
             p.bounds[E] = S;
             p.ntile_prefix[E] = tiles;
+            p.pad_start[E] = padded;
             p.hdr[kHdrTiles] = tiles;
         }
     }
@@ -716,16 +762,16 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
         if (e >= 0) {
             const int pos = s_row[warp * E + e] + rank;
             p.ids_dst[pos] = i;
-            p.ids_src[pos] = p.per_slot ? i : i / k;
+            p.slot_prow[i] = pos + s_delta[e];
         }
         __syncthreads();
     }
     // round the CTA's rows, four planes of a row to a warp at a time
-    const int planes = (p.n_in + 255) / 256, chunks = (planes + kMxPlanes - 1) / kMxPlanes;
+    const int planes = (p.n_in + 255) / 256, chunks = (planes + kMxPlanes - 1) / kMxPlanes, copies = p.per_slot ? 1 : k;
     const int dr = 32 / chunks, dc = 32 % chunks;
     int64_t r = r0 + warp / chunks;
     for (int c = warp % chunks; r < r1; r += dr) {
-        round_planes<TYPE>(p.x, r, p.n_in, c * kMxPlanes, planes, p.rows, lane);
+        round_planes<TYPE>(p.x, r, p.n_in, c * kMxPlanes, planes, p.slot_prow + r * copies, copies, p.rows, lane);
         c += dc;
         if (c >= chunks) {
             c -= chunks;
@@ -1231,7 +1277,7 @@ bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done) {
 template <int TYPE>
 moe_status launch_place(const MxPlaceArgs& a, unsigned grid, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    if (!allow_smem(mx4_place_kernel<TYPE>, (int)(33 * kRidMaxE * sizeof(int)), done)) return MOE_ERR_CUDA;
+    if (!allow_smem(mx4_place_kernel<TYPE>, (int)(34 * kRidMaxE * sizeof(int)), done)) return MOE_ERR_CUDA;
     return launch_dependent(mx4_place_kernel<TYPE>, grid, kMpThreads, smem, s, a);
 }
 
@@ -1247,9 +1293,9 @@ moe_status launch_decode(const MxDecodeArgs& a, cudaStream_t s) {
 moe_status launch_mx4_gemm(const Mx4Params& p, int64_t max_coltiles, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     if (!allow_smem(mx4_gemm_kernel, (int)kMxSmem, done)) return MOE_ERR_CUDA;
-    const int64_t units = max_coltiles * ((p.L.mt_count + p.tiles_per_unit - 1) / p.tiles_per_unit);
-    const int sms = mx_sm_count();
-    const unsigned grid = (unsigned)(units < sms ? units : sms);
+    const int64_t units = max_coltiles * ((p.L.mt_count + 1) / 2);
+    const int pairs = mx_sm_count() / 2;
+    const unsigned grid = 2u * (unsigned)(units < pairs ? units : pairs);
     return launch_dependent(mx4_gemm_kernel, grid, kMxThreads, kMxSmem, stream, p);
 }
 
@@ -1309,13 +1355,15 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
         prof_mark(s, "decode");
         return st;
     }
-    // the rounded rows take the place of the 16-bit ones (128 bytes per 64 values)
+    // The rounded rows take the workspace of the 16-bit ones: 128 bytes per 256
+    // values and 4 per 128 where those take 128 per 64.  Only up to 64 values do
+    // the scales not fit behind the codes; there they take the rows' factors.
     MxRows o;
-    o.pitch = p.L.kt_count * 32;
-    o.scale_pitch = planes * 8;
-    const int64_t rows = mode == MOE_BROADCAST ? n_tokens : S;
+    o.rows_pad = W.rows_pad;
+    o.scale_ld = (W.rows_pad + 3) / 4 * 4;  // bulk copies start on 16 bytes
     o.codes = (uint8_t*)(ws + W.xt);
-    o.scales = o.codes + rows * o.pitch;
+    o.scales = n_in <= kTileK ? (uint32_t*)(ws + W.xs)
+                              : (uint32_t*)(o.codes + (size_t)planes * W.rows_pad * 128u);
     const bool broadcast = mode == MOE_BROADCAST;
     prof_begin(s);
     moe_status st;
@@ -1326,10 +1374,11 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
         prof_mark(s, "row_ids");
         MxPlaceArgs a = {ids, x, n_in, n_tokens, k, n_experts, !broadcast, counts, (int32_t*)(ws + W.bounds),
-                         (int32_t*)(ws + W.tiles), (int32_t*)(ws + W.src1), (int32_t*)(ws + W.dst), hdr, o};
+                         (int32_t*)(ws + W.tiles), (int32_t*)(ws + W.pad), (int32_t*)(ws + W.dst),
+                         (int32_t*)(ws + W.sprow), hdr, o};
         const int Ep = (n_experts + 31) & ~31;
-        const size_t ranks = 32 * (size_t)n_experts, sums = 2 * (size_t)(kMpThreads / Ep) * Ep;
-        const size_t smem = ((size_t)n_experts + (ranks > sums ? ranks : sums)) * sizeof(int);
+        const size_t rows = 32 * (size_t)n_experts, sums = 2 * (size_t)(kMpThreads / Ep) * Ep;
+        const size_t smem = (2 * (size_t)n_experts + (rows > sums ? rows : sums)) * sizeof(int);
         st = x_type == MOE_BF16  ? launch_place<MOE_BF16>(a, G, smem, s)
              : x_type == MOE_F16 ? launch_place<MOE_F16>(a, G, smem, s)
                                  : launch_place<MOE_F32>(a, G, smem, s);
@@ -1340,24 +1389,25 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
                             (int32_t*)(ws + W.pad), (int32_t*)(ws + W.sprow), kMxBN, hdr, nullptr, s, &n_rid);
         if (st) return st;
         prof_mark(s, "row_ids", n_rid);
-        const int64_t blocks = (rows + 7) / 8, cap = (int64_t)mx_sm_count() * 8;
+        const int64_t rows = broadcast ? n_tokens : S, blocks = (rows + 7) / 8, cap = (int64_t)mx_sm_count() * 8;
         const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
-        if (x_type == MOE_BF16) mx4_round_kernel<MOE_BF16><<<grid, 256, 0, s>>>(x, n_in, rows, o, hdr);
-        else if (x_type == MOE_F16) mx4_round_kernel<MOE_F16><<<grid, 256, 0, s>>>(x, n_in, rows, o, hdr);
-        else mx4_round_kernel<MOE_F32><<<grid, 256, 0, s>>>(x, n_in, rows, o, hdr);
+        const int32_t* prow = (const int32_t*)(ws + W.sprow);
+        const int copies = broadcast ? k : 1;
+        if (x_type == MOE_BF16) mx4_gather_kernel<MOE_BF16><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
+        else if (x_type == MOE_F16) mx4_gather_kernel<MOE_F16><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
+        else mx4_gather_kernel<MOE_F32><<<grid, 256, 0, s>>>(x, n_in, prow, copies, rows, o, hdr);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (st) return st;
-    prof_mark(s, "round");
-    p.tiles_per_unit = 2;
+    prof_mark(s, "gather");
     p.n_groups = n_experts;
     p.bounds = (const int32_t*)(ws + W.bounds);
     p.ntile_prefix = (const int32_t*)(ws + W.tiles);
+    p.pad_start = (const int32_t*)(ws + W.pad);
     p.B = o.codes;
     p.BS = o.scales;
-    p.b_pitch = o.pitch;
-    p.bs_pitch = o.scale_pitch;
-    p.src_rows = (const int32_t*)(ws + W.src1);
+    p.rows_pad = o.rows_pad;
+    p.scale_ld = o.scale_ld;
     p.dst_rows = (const int32_t*)(ws + W.dst);
     st = launch_mx4_gemm(p, (S + kMxBN - 1) / kMxBN + (S < n_experts ? S : n_experts), s);
     prof_mark(s, "gemm");
