@@ -84,9 +84,6 @@ inline int64_t tiled_rows(int64_t S, int n_groups) {
 // offsets in the workspace: 2 * kRidMaxCtas * E + E words.
 constexpr int kRidMaxCtas = 64;
 constexpr int kRidMaxE = 1024;
-// The 4-bit product's counting launch keeps kMxPlaceCtas * E counts there.
-constexpr int kMxPlaceCtas = 148;
-constexpr int kRidWords = 2 * kRidMaxCtas + 1 > kMxPlaceCtas ? 2 * kRidMaxCtas + 1 : kMxPlaceCtas;
 struct WsLayout {
     int64_t S, rows_pad, rows_pad_sh;
     size_t hdr, rid, src1, dst, sprow, bounds, active, tiles, pad, h, h_sh, xt, xt_sh, xs, xs_sh, total;
@@ -105,7 +102,7 @@ struct WsLayout {
         dst = o; o += up(S * 4);
         sprow = o; o += up(S * 4);  // tiled row of each slot t*k+s
         bounds = o; o += up((size_t)(n_experts + 1) * 4);
-        rid = o; o += n_experts <= kRidMaxE ? up((size_t)kRidWords * n_experts * 4) : 0;
+        rid = o; o += n_experts <= kRidMaxE ? up(((size_t)2 * kRidMaxCtas * n_experts + n_experts) * 4) : 0;
         active = o; o += up((size_t)(n_experts + 1) * 4);
         tiles = o; o += up((size_t)(n_experts + 1) * 4);
         pad = o; o += up((size_t)(n_experts + 1) * 4);
@@ -113,7 +110,7 @@ struct WsLayout {
         h_sh = o; o += up(hs_gemv > hs_gemm ? hs_gemv : hs_gemm);
         xt = o; o += up((size_t)rows_pad * kin * 128);
         xt_sh = o; o += n_hidden_sh > 0 ? up((size_t)rows_pad_sh * kin * 128) : 0;
-        xs = o; o += up((size_t)rows_pad * 4);  // power-of-two scale of each tiled activation row
+        xs = o; o += up((size_t)rows_pad * 8);  // power-of-two scale of each tiled activation row (4-bit: scale bytes)
         xs_sh = o; o += n_hidden_sh > 0 ? up((size_t)rows_pad_sh * 4) : 0;
         total = o;
     }

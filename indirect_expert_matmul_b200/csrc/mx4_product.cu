@@ -55,7 +55,7 @@ constexpr uint32_t kMxCodes = kTileM * 32;                 // codes of a tile's 
 constexpr uint32_t kMxACodes = kMxStageKt * kMxCodes;      // 16384
 constexpr uint32_t kMxAScales = kMxStageKt * kTileM * 2;   // 1024
 constexpr uint32_t kMxB = kMxBN / 2 * 128;                 // 12288: half the rows
-constexpr uint32_t kMxBScales = 2 * kMxBN * 4;             // 1536: every row's two words
+constexpr uint32_t kMxBScales = kMxBN * 8;                 // 1536: every row's two words
 constexpr uint32_t kMxOffB = kMxACodes, kMxOffAS = kMxOffB + kMxB, kMxOffBS = kMxOffAS + kMxAScales;
 constexpr uint32_t kMxStagePitch = (kMxOffBS + kMxBScales + 1023) / 1024 * 1024;
 constexpr uint32_t kMxBarOff = kMxStages * kMxStagePitch;
@@ -76,7 +76,7 @@ struct Mx4Params {
     int n_groups;
     const int32_t *bounds, *ntile_prefix, *pad_start;
     const uint8_t* B;               // codes [plane][rows_pad][128]
-    const uint32_t* BS;             // scales [K / 128][scale_ld]
+    const uint2* BS;                // scales [plane][scale_ld]
     int64_t rows_pad, scale_ld;
     const int32_t* dst_rows;
     float* out;
@@ -285,21 +285,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
             if (!ok) break;
             const uint32_t nh = (uint32_t)(u.n + 31) / 32u * 16u;
             const uint8_t* bsrc = p.B + (size_t)(u.p0pad + (int)(rank * nh)) * 128u;
-            const uint32_t* ssrc = p.BS + u.p0pad;
+            const uint2* ssrc = p.BS + u.p0pad;
             for (int ks = 0; ks < KS; ++ks, ++q) {
                 ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 if (issue && !((int)blockIdx.x == p.stall_cta && q == p.stall_stage)) {
                     uint8_t* st = smem + s * kMxStagePitch;
-                    const bool two = KT - ks * kMxStageKt > 2;  // the stage's second 128 values
-                    ptx::mbar_arrive_expect_tx(&full[s], nh * 128u + (two ? nh * 16u : nh * 8u));
+                    ptx::mbar_arrive_expect_tx(&full[s], nh * 144u);
                     ptx::bulk_g2s(st + kMxOffB, bsrc, nh * 128u, &full[s]);
-                    ptx::bulk_g2s(st + kMxOffBS, ssrc, nh * 8u, &full[s]);
-                    if (two) ptx::bulk_g2s(st + kMxOffBS + kMxBN * 4, ssrc + p.scale_ld, nh * 8u, &full[s]);
+                    ptx::bulk_g2s(st + kMxOffBS, ssrc, nh * 16u, &full[s]);
                 }
                 __syncwarp();
                 bsrc += (size_t)p.rows_pad * 128u;
-                ssrc += 2 * p.scale_ld;
+                ssrc += p.scale_ld;
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
         }
@@ -386,14 +384,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                 if (!ok) break;
                 if (++old == kMxStages) { old = 0; old_ph ^= 1; }
                 const uint32_t as = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffAS);
-                const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 4;
+                const uint32_t bs = ptx::smem_u32(smem + s * kMxStagePitch + kMxOffBS) + lane * 8;
                 uint32_t v[8], w[16];
                 weight_scales(as, lane, v);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        w[h * 8 + c] = c < kMxBN / 32 ? ptx::lds32(bs + h * (kMxBN * 4) + c * 128) : 0u;
+                for (int c = 0; c < 8; ++c) {
+                    const uint2 q = c < kMxBN / 32 ? ptx::lds64(bs + c * 256) : make_uint2(0u, 0u);
+                    w[c] = q.x;
+                    w[8 + c] = q.y;
+                }
                 ptx::tc_fence_after();
                 ptx::tmem_st_32x32b_x8(dst + (uint32_t)slot * kMxScaleCols, v);
                 ptx::tmem_st_32x32b_x16(dst + (uint32_t)slot * kMxScaleCols + 8u, w);
@@ -470,11 +469,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
 
 // -------------------------------------------------------- quantising gather
 // Where the rounded rows go: codes [plane of 256 values][row][128 bytes], the
-// 16-byte chunk of block c at c ^ (row % 8); scales [128 values][row], a word
-// of four scale bytes.
+// 16-byte chunk of block c at c ^ (row % 8); scales [plane][row], two words of
+// four scale bytes.
 struct MxRows {
     uint8_t* codes;
-    uint32_t* scales;
+    uint2* scales;
     int64_t rows_pad, scale_ld;
 };
 
@@ -518,8 +517,13 @@ struct MxEight {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (TYPE == MOE_BF16) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                    // scaled as bf16 pairs: a power of two, exact where the result rounds to a
+                    // code other than 0
+                    const uint32_t p = (__float_as_uint(inv) >> 16) * 0x10001u;
+                    const __nv_bfloat162 q = __hmul2(*(const __nv_bfloat162*)&w[i], *(const __nv_bfloat162*)&p);
+                    const uint32_t u = *(const uint32_t*)&q;
+                    v[2 * i] = __uint_as_float(u << 16);
+                    v[2 * i + 1] = __uint_as_float(u & 0xffff0000u);
                 } else {
                     const float2 f = __half22float2(*(const __half2*)&w[i]);
                     v[2 * i] = f.x;
@@ -527,52 +531,57 @@ struct MxEight {
                 }
             }
         }
-        return mx_codes8(v, inv);
+        return mx_codes8(v, TYPE == MOE_BF16 ? 1.f : inv);
     }
 };
 
 constexpr int kMxPlanes = 4;  // planes of a row a warp has in flight
 
-// Planes kp0 .. kp0 + 3 (256 values each) of source row r by one warp, eight
-// values a lane, four lanes a block, to the tile rows prow[0 .. copies).
+// Planes kp0 .. kp0 + 3 (256 values each) of source row r by one warp, two
+// planes at a time, sixteen values a lane and two lanes a block, to the tile
+// rows prow[0 .. copies).  (Instructions are the bound next to the bytes: eight
+// values a lane took half as many again.)
 template <int TYPE>
 __device__ __forceinline__ void round_planes(const void* __restrict__ x, int64_t r, int n_in, int kp0, int planes,
                                              const int32_t* prow, int copies, const MxRows& o, int lane) {
-    constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
-    const int col = kp0 * 256 + lane * 8;
+    constexpr int esz = TYPE == MOE_F32 ? 4 : 2, kPairs = kMxPlanes / 2;
+    const int col = kp0 * 256 + lane * 16;
     const char* src = (const char*)x + (r * n_in + col) * esz;
-    MxEight<TYPE> v[kMxPlanes];
+    MxEight<TYPE> v[kPairs][2];
 #pragma unroll
-    for (int i = 0; i < kMxPlanes; ++i) {
-        if (col + i * 256 < n_in) v[i].load(src + i * 256 * esz);
-        else v[i].zero();
-    }
-    uint32_t w[kMxPlanes], sw[kMxPlanes];
+    for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-    for (int i = 0; i < kMxPlanes; ++i) {
-        uint32_t m = v[i].amax_bits();
+        for (int h = 0; h < 2; ++h) {
+            if (col + i * 512 < n_in) v[i][h].load(src + (i * 512 + h * 8) * esz);
+            else v[i][h].zero();
+        }
+    uint2 w[kPairs], sw[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        uint32_t m = max(v[i][0].amax_bits(), v[i][1].amax_bits());
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         const uint32_t X = mx_scale_byte(m);
-        w[i] = X == 255u ? 0u : v[i].codes(mx_inv_scale(X));
-        sw[i] = X << (8 * ((lane >> 2) & 3));  // the scales of this half's four blocks in one word
-        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 4);
-        sw[i] |= __shfl_xor_sync(0xffffffffu, sw[i], 8);
+        const float inv = mx_inv_scale(X);
+        w[i] = X == 255u ? make_uint2(0u, 0u) : make_uint2(v[i][0].codes(inv), v[i][1].codes(inv));
+        uint32_t half = X << (8 * ((lane >> 1) & 3));  // the scales of 128 values' four blocks in one word
+        half |= __shfl_xor_sync(0xffffffffu, half, 2);
+        half |= __shfl_xor_sync(0xffffffffu, half, 4);
+        sw[i] = make_uint2(half, __shfl_xor_sync(0xffffffffu, half, 8));  // (lanes 0 and 16: the plane's two)
     }
+    const int kp = kp0 + (lane >> 4);
     const size_t pitch = (size_t)o.rows_pad * 128u;
-    uint8_t* plane = o.codes + (size_t)kp0 * pitch + (lane & 3) * 4;
-    uint32_t* sp = o.scales + (size_t)(2 * kp0 + (lane >> 4)) * o.scale_ld;
-    const bool sc = (lane & 15) == 0;
+    uint8_t* plane = o.codes + (size_t)kp * pitch + (lane & 1) * 8;
+    uint2* sp = o.scales + (size_t)kp * o.scale_ld;
     for (int j = 0; j < copies; ++j) {
         const uint32_t pr = (uint32_t)prow[j];
-        uint8_t* c = plane + ((size_t)pr * 128u + (((uint32_t)(lane >> 2) ^ (pr & 7u)) << 4));
-        uint32_t* q = sp + pr;
+        uint8_t* c = plane + ((size_t)pr * 128u + ((((uint32_t)(lane >> 1) ^ pr) & 7u) << 4));
+        uint2* q = sp + pr;
 #pragma unroll
-        for (int i = 0; i < kMxPlanes; ++i) {
-            if (kp0 + i < planes) *(uint32_t*)c = w[i];
-            if (sc && col + i * 256 < n_in) *q = sw[i];
-            c += pitch;
-            q += 2 * o.scale_ld;
+        for (int i = 0; i < kPairs; ++i) {
+            if (kp + 2 * i < planes) {
+                *(uint2*)(c + 2 * i * pitch) = w[i];
+                if ((lane & 15) == 0) q[2 * i * o.scale_ld] = sw[i];
+            }
         }
     }
 }
@@ -595,29 +604,43 @@ mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restric
 // ------------------------------------------- row ids and gather in two launches
 // For up to kRidMaxE experts the tables come from two launches instead of the
 // row-id pass and a gather (35 + 60 us of a 4096-token gate product, 32 + 98 us
-// of the skewed 8192-token one): G CTAs count their tokens' slots by expert;
-// then each CTA sums the counts before its own (the place of its first slot of
-// every expert, the tables' prefixes), ranks its slots in slot order - the same
-// stable counting sort - and rounds its rows straight into their tile rows.
-// The second launch starts while the first runs and fetches its rows into L2.
+// of the skewed 8192-token one): one counts the slots of each chunk of tokens by
+// expert; in the other each CTA, one of kMpParts of a chunk, sums the counts
+// before its own (the place of its first slot of every expert, the tables'
+// prefixes), ranks its slots in slot order - the same stable counting sort -
+// and rounds its rows straight into their tile rows.  The second launch starts
+// while the first runs, with the count of its chunk's slots before its own.
+// (With a count for every CTA, all of them reading 148 counts an expert took
+// 6.7 us.)
 constexpr int kMpThreads = 1024;
-constexpr int64_t kMpPrefetch = 512 * 1024;
+constexpr int kMpMaxCtas = 148, kMpParts = 4;
+static_assert((kMpMaxCtas + kMpParts - 1) / kMpParts <= 2 * kRidMaxCtas, "counts take the row-id pass's scratch");
 
 __device__ __forceinline__ int64_t mp_token(int64_t T, int g, int G) { return T * g / G; }
 
+// Count slots [s0, s1) by expert into cnt (shared; integers: the order does not
+// matter).  An id outside [0, E) is left out; true where one was met.
+__device__ __forceinline__ bool count_slots(const int32_t* __restrict__ ids, int s0, int s1, int E, int* cnt) {
+    bool bad = false;
+    for (int i = s0 + threadIdx.x; i < s1; i += kMpThreads) {
+        const int e = __ldg(ids + i);
+        if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);
+        else bad = true;
+    }
+    return bad;
+}
+
+// CTA c: the chunk of tokens of place CTAs [c * kMpParts, (c + 1) * kMpParts) of G.
 __global__ void __launch_bounds__(kMpThreads)
-mx4_count_kernel(const int32_t* __restrict__ ids, int64_t T, int k, int E, int32_t* __restrict__ counts, int* hdr) {
+mx4_count_kernel(const int32_t* __restrict__ ids, int64_t T, int k, int E, int G, int32_t* __restrict__ counts, int* hdr) {
     extern __shared__ int s_cnt[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (__syncthreads_or(threadIdx.x == 0 && read_status(hdr + kHdrStatus) != 0)) return;
     for (int e = threadIdx.x; e < E; e += kMpThreads) s_cnt[e] = 0;
     __syncthreads();
-    const int s0 = (int)(mp_token(T, blockIdx.x, gridDim.x) * k), s1 = (int)(mp_token(T, blockIdx.x + 1, gridDim.x) * k);
-    for (int i = s0 + threadIdx.x; i < s1; i += kMpThreads) {
-        const int e = __ldg(ids + i);
-        if ((unsigned)e < (unsigned)E) atomicAdd(&s_cnt[e], 1);  // a count: the order does not matter
-        else set_status(hdr + kHdrStatus, MOE_ERR_BAD_ID);
-    }
+    const int g0 = blockIdx.x * kMpParts;
+    if (count_slots(ids, (int)(mp_token(T, g0, G) * k), (int)(mp_token(T, min(g0 + kMpParts, G), G) * k), E, s_cnt))
+        set_status(hdr + kHdrStatus, MOE_ERR_BAD_ID);
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kMpThreads) counts[(size_t)blockIdx.x * E + e] = s_cnt[e];
 }
@@ -656,21 +679,17 @@ template <int TYPE>
 __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs p) {
     extern __shared__ int s_dyn[];
     const int E = p.E, G = gridDim.x, g = blockIdx.x, k = p.k;
-    int* s_base = s_dyn;        // [E] sorted position of the CTA's next slot of the expert
+    int* s_base = s_dyn;        // [E] slots of the chunk before the CTA's, then the position of its next slot
     int* s_delta = s_base + E;  // [E] tile row minus sorted position
     int* s_row = s_delta + E;   // [32][E] a warp's counts, then its first positions
     __shared__ int s_sums[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t t0 = mp_token(p.T, g, G), t1 = mp_token(p.T, g + 1, G);
     const int64_t r0 = p.per_slot ? t0 * k : t0, r1 = p.per_slot ? t1 * k : t1;
-    {  // the CTA's source rows into L2, in pieces of up to 64 KB on 16-byte borders
-        constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
-        const char* a = (const char*)p.x + r0 * p.n_in * esz;
-        // (no more than fits in L2 for all CTAs together)
-        const int64_t all = (r1 - r0) * p.n_in * esz, bytes = all < kMpPrefetch ? all : kMpPrefetch;
-        const int64_t off = (int64_t)tid * 65536;
-        if (off < bytes) ptx::bulk_prefetch_l2(a + off, (uint32_t)(bytes - off < 65536 ? bytes - off : 65536));
-    }
+    for (int e = tid; e < E; e += kMpThreads) s_base[e] = 0;
+    __syncthreads();
+    const int chunk = g / kMpParts, C = (G + kMpParts - 1) / kMpParts;
+    count_slots(p.ids, (int)(mp_token(p.T, chunk * kMpParts, G) * k), (int)(t0 * k), E, s_base);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (read_status(p.hdr + kHdrStatus) != 0) return;
@@ -681,20 +700,20 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
         const int e = tid % Ep, part = tid / Ep;
         if (part < parts && e < E) {
             int c = part;
-            for (; c + 7 * parts < G; c += 8 * parts) {
+            for (; c + 7 * parts < C; c += 8 * parts) {
                 int v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = __ldcg(p.counts + (size_t)(c + i * parts) * E + e);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     all += v[i];
-                    before += c + i * parts < g ? v[i] : 0;
+                    before += c + i * parts < chunk ? v[i] : 0;
                 }
             }
-            for (; c < G; c += parts) {
+            for (; c < C; c += parts) {
                 const int v = __ldcg(p.counts + (size_t)c * E + e);
                 all += v;
-                before += c < g ? v : 0;
+                before += c < chunk ? v : 0;
             }
         }
         // s_row has room for parts * 2 <= 64 rows of Ep <= 1024 / parts words
@@ -716,7 +735,7 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
         const int q = cta_prefix((all + kMxBN - 1) / kMxBN, s_sums, &tiles);
         const int pad = cta_prefix((all + 7) & ~7, s_sums, &padded);
         if (tid < E) {
-            s_base[tid] = b + before;
+            s_base[tid] += b + before;
             s_delta[tid] = pad - b;
             if (g == 0) {
                 p.bounds[tid] = b;
@@ -1356,21 +1375,21 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
         return st;
     }
     // The rounded rows take the workspace of the 16-bit ones: 128 bytes per 256
-    // values and 4 per 128 where those take 128 per 64.  Only up to 64 values do
+    // values and 8 of scales where those take 128 per 64.  Only up to 64 values do
     // the scales not fit behind the codes; there they take the rows' factors.
     MxRows o;
     o.rows_pad = W.rows_pad;
     o.scale_ld = (W.rows_pad + 3) / 4 * 4;  // bulk copies start on 16 bytes
     o.codes = (uint8_t*)(ws + W.xt);
-    o.scales = n_in <= kTileK ? (uint32_t*)(ws + W.xs)
-                              : (uint32_t*)(o.codes + (size_t)planes * W.rows_pad * 128u);
+    o.scales = n_in <= kTileK ? (uint2*)(ws + W.xs) : (uint2*)(o.codes + (size_t)planes * W.rows_pad * 128u);
     const bool broadcast = mode == MOE_BROADCAST;
     prof_begin(s);
     moe_status st;
     if (n_experts <= kRidMaxE) {
-        const unsigned G = (unsigned)(n_tokens < kMxPlaceCtas ? n_tokens : kMxPlaceCtas);
+        const unsigned G = (unsigned)(n_tokens < kMpMaxCtas ? n_tokens : kMpMaxCtas);
         int32_t* counts = (int32_t*)(ws + W.rid);
-        mx4_count_kernel<<<G, kMpThreads, (size_t)n_experts * sizeof(int), s>>>(ids, n_tokens, k, n_experts, counts, hdr);
+        mx4_count_kernel<<<(G + kMpParts - 1) / kMpParts, kMpThreads, (size_t)n_experts * sizeof(int), s>>>(
+            ids, n_tokens, k, n_experts, (int)G, counts, hdr);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
         prof_mark(s, "row_ids");
         MxPlaceArgs a = {ids, x, n_in, n_tokens, k, n_experts, !broadcast, counts, (int32_t*)(ws + W.bounds),
