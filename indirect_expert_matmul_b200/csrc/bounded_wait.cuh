@@ -11,15 +11,17 @@ namespace moe {
 constexpr long long kWaitLimitCycles = 1ll << 32; // ~2 s
 constexpr uint32_t kSleepNs = 20000; // upper bound of one hardware wait
 
-// Bounded wait by one lane; false when the kernel is aborting.  The lane
+// Bounded wait by one lane (CLUSTER: of arrivals by another CTA too); false when the kernel is aborting.  The lane
 // sleeps in hardware between polls (suspend-time hint), so waiting roles do
 // not take issue slots from the dequantisation warps.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
                                          long long limit) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (!CLUSTER && ptx::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
-        if (ptx::mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
+        if (CLUSTER ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait_sleep(bar, parity, kSleepNs))
+            return true;
         if (*abort_flag) return false;
         if (clock64() - t0 > limit) {
             *abort_flag = 1;

@@ -317,30 +317,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         }
     } else if (warp == 1 && rank == 0) {
         // -------------------------------------------------------------- MMAs
-        const uint32_t issue = ptx::elect_one(), smem_a = ptx::smem_u32(smem);
-        int s = 0, slot = 0;
-        uint32_t ph = 0, use = 0;
-        bool ok = true;
-        for (int t = pair; t < total && ok; t += pairs, ++use) {
-            MxTile u;
-            ok = take_unit((int)use, u);
-            if (!ok) break;
-            const int n32 = (u.n + 31) & ~31;
-            const uint32_t id0 = ptx::idesc_mxf4(n32, 0, 256), id1 = ptx::idesc_mxf4(n32, 1, 256), buf = use & 1;
-            const uint32_t d = tmem + buf * kMxBN;
-            ok = warp_wait<true>(&acc_empty[buf], ((use >> 1) & 1) ^ 1, abort_flag, status, p.wait_limit);
-            if (!ok) break;
-            for (int ks = 0; ks < KS; ++ks) {
-                // (the scale warps of both CTAs arrive after they have seen the stage's copies land)
-                ok = warp_wait<true>(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+        // One thread's loop: a stage's cycles here are the bound where the clock is low
+        // (the power limit), so the next stage is asked for before this one's MMAs.
+        if (ptx::elect_one()) {
+            const uint32_t smem_a = ptx::smem_u32(smem);
+            int s = 0, slot = 0;
+            uint32_t ph = 0, use = 0;
+            bool ok = true, ready = false;
+            for (int t = pair; t < total && ok; t += pairs, ++use) {
+                const int k = (int)use % kMxUnits;
+                ok = wait_bar(&unit_full[k], (use / kMxUnits) & 1u, abort_flag, status, p.wait_limit);
                 if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t st = smem_a + (uint32_t)s * kMxStagePitch;
-                const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)slot * kMxScaleCols;
-                const uint64_t ad = ptx::desc_k_sw32(st), bd = ptx::desc_k_sw128(st + kMxOffB);
-                const int kts = KT - ks * kMxStageKt;
-                if (issue) {
-                    // one branch for all of a stage's MMAs: a predicate on each cost ~80 cycles an MMA
+                const int n32 = (s_unit[k].n + 31) & ~31;
+                ptx::mbar_arrive(&unit_empty[k]);
+                const uint32_t id0 = ptx::idesc_mxf4(n32, 0, 256), id1 = ptx::idesc_mxf4(n32, 1, 256), buf = use & 1;
+                const uint32_t d = tmem + buf * kMxBN;
+                ok = wait_bar<true>(&acc_empty[buf], ((use >> 1) & 1) ^ 1, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                for (int ks = 0; ks < KS; ++ks) {
+                    // (the scale warps of both CTAs arrive after they have seen the stage's copies land)
+                    ok = ready || wait_bar<true>(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t st = smem_a + (uint32_t)s * kMxStagePitch;
+                    const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)slot * kMxScaleCols;
+                    const uint64_t ad = ptx::desc_k_sw32(st), bd = ptx::desc_k_sw128(st + kMxOffB);
+                    const int kts = KT - ks * kMxStageKt;
+                    uint64_t* done = &empty[s];
+                    if (++s == kMxStages) { s = 0; ph ^= 1; }
+                    if (++slot == kMxScaleSlots) slot = 0;
+                    ready = ptx::mbar_try_wait_cluster(&sf_full[s], ph);
                     auto step = [&](int j) {  // address fields count 16 bytes; sums stay inside their 14 bits
                         ptx::mma_mxf4_pair(d, ad + (j * kMxCodes >> 4), bd + j * 2, j & 1 ? id1 : id0, sf + (j >> 1) * 4,
                                            sf + 8 + (j >> 1) * 8, (ks | j) != 0);
@@ -351,18 +357,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                     } else {
                         for (int j = 0; j < kts; ++j) step(j);
                     }
-                    ptx::mma_commit_pair(&empty[s]);
+                    ptx::mma_commit_pair(done);
                 }
-                __syncwarp();
-                if (++s == kMxStages) { s = 0; ph ^= 1; }
-                if (++slot == kMxScaleSlots) slot = 0;
+                if (!ok) break;
+                ptx::mma_commit_pair(&acc_full[buf]);
             }
-            if (!ok) break;
-            if (issue) ptx::mma_commit_pair(&acc_full[buf]);
-            __syncwarp();
-        }
-        // every MMA issued has completed before the CTAs can release tensor memory
-        if (issue) {
+            // every MMA issued has completed before the CTAs can release tensor memory
             ptx::mma_commit_pair(drained);
             volatile int never = 0;
             wait_bar(drained, 0, &never, status, p.wait_limit);
