@@ -985,7 +985,9 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
     ptx::tc_fence_after();
     const uint32_t tmem = uniform(s_tmem);
     const int items = uniform(s_groups) * MT;
-    const int it0 = (int)((int64_t)items * blockIdx.x / gridDim.x), it1 = (int)((int64_t)items * (blockIdx.x + 1) / gridDim.x);
+    // (rounded up: CTA 0 has the first item however few there are)
+    const int it0 = (int)(((int64_t)items * blockIdx.x + gridDim.x - 1) / gridDim.x);
+    const int it1 = (int)(((int64_t)items * (blockIdx.x + 1) + gridDim.x - 1) / gridDim.x);
 
     if (warp == 0) {
         // ------------------------------------------------------------ weights

@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const Route
         const int G = p.n_groups;
         const bool exact = !BIAS && p.group_top == 1;  // the groups' best logits, compared as they are
         auto group_key = [&](int j) { return BIAS ? __fadd_rn(s[j], b[j]) : exact ? l[j] : s[j]; };
-        float mine = -INFINITY;  // lane g: the score of group g
+        float mine = -INFINITY, mag = 0.f;  // lane g: the score of group g, what its terms' roundings scale with
         const int P = size / NPL;
         const bool lanes = P * NPL == size && (P & (P - 1)) == 0;
         if (lanes) {
@@ -340,11 +340,13 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const Route
             const float sc = p.group_top == 2 ? __fadd_rn(a, c) : a;
             mine = __shfl_sync(0xffffffffu, sc, lane < G ? lane * P : 0);
             if (lane >= G) mine = -INFINITY;
+            if (BIAS && p.group_top == 2) mag = fabsf(a) + fabsf(c);
         } else {
             for (int g = 0; g < G; ++g) {
                 float a, c;
                 group_top2<NPL>(group_key, lane, E, size, g, a, c);
                 if (lane == g) mine = p.group_top == 2 ? __fadd_rn(a, c) : a;
+                if (BIAS && p.group_top == 2) mag = fmaxf(mag, fabsf(a) + fabsf(c));
             }
         }
         int rank = 0;  // groups ahead of this lane's
@@ -358,7 +360,10 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const Route
             const uint32_t u = ordered(mine);
             const uint32_t lo = __reduce_min_sync(0xffffffffu, in ? u : 0xffffffffu);
             const uint32_t hi = __reduce_max_sync(0xffffffffu, lane < G && !in ? u : 0u);
-            if (hi >= rival(lo, 2.f * err) && lo > ordered(-INFINITY)) {
+            // (a sum of two keys of opposite sign: each rounded as large as it is)
+            const float own = mag < INFINITY ? mag : 0.f;
+            const float terms = 1.2e-7f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(own)));
+            if (hi >= rival(lo, 2.f * err + terms) && lo > ordered(-INFINITY)) {
                 exact64.fill(lane);
                 const double best = exact64.group_score(lane, size);
                 rank = 0;

@@ -59,6 +59,115 @@ def test_product(mode, T, E, k, n_in, n_out, dtype):
     _check(blocks, x, _ids(T, k, E, T + E), mode)
 
 
+@pytest.mark.parametrize("T", [3, 150])
+@pytest.mark.parametrize("n_out", [16, 47, 48, 80, 112, 128, 144, 208, 256, 272, 368])
+def test_every_kind_of_last_tile(T, n_out):
+    # last tiles of 16 to 112 rows (32-row sub-blocks, a 16-row one, both), odd and even tile counts
+    blocks = _weights(3, n_out, 192, n_out)
+    x = torch.randn(T, 192, generator=torch.Generator().manual_seed(T)).bfloat16().cuda()
+    _check(blocks, x, _ids(T, 2, 3, n_out), "broadcast")
+
+
+@pytest.mark.parametrize("n_in", [32, 64, 96, 128, 160, 224, 256, 288, 480, 512, 544, 1056])
+def test_every_kind_of_last_stage(n_in):
+    blocks = _weights(2, 40, n_in, n_in)
+    for T in (2, 140):
+        x = torch.randn(T, n_in, generator=torch.Generator().manual_seed(n_in)).cuda()
+        _check(blocks, x, _ids(T, 2, 2, n_in), "broadcast")
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 300, 10), (33, 1100, 9), (20, 1100, 8), (300, 1024, 2)])
+def test_many_experts(T, E, k):
+    # tables read from memory (more than 256 experts) and the general row-id pass (more than 1024)
+    blocks = _weights(E, 24, 64, E)
+    x = torch.randn(T, 64, generator=torch.Generator().manual_seed(E)).bfloat16().cuda()
+    _check(blocks, x, _ids(T, k, E, T), "broadcast")
+
+
+@pytest.mark.parametrize("T,n_in", [(2, 9216), (2, 9248), (1, 12320)])
+def test_long_rows(T, n_in):
+    # the longest that the one-launch form holds in shared memory, and past it
+    blocks = _weights(2, 20, n_in, n_in)
+    x = torch.randn(T, n_in, generator=torch.Generator().manual_seed(n_in)).bfloat16().cuda()
+    _check(blocks, x, _ids(T, 2, 2, 1), "broadcast")
+
+
+@pytest.mark.parametrize("S", [31, 32, 33, 255, 256, 257])
+def test_slot_counts_at_the_borders_of_the_forms(S):
+    blocks = _weights(5, 36, 96, S)
+    x = torch.randn(S, 96, generator=torch.Generator().manual_seed(S)).cuda()
+    ids = torch.randint(0, 5, (S, 1), generator=torch.Generator().manual_seed(S), dtype=torch.int32)
+    _check(blocks, x, ids, "broadcast")
+    few = ids.clone()
+    few[:] = 2
+    few[S // 2] = 4
+    _check(blocks, x, few, "per_slot")
+
+
+@pytest.mark.parametrize("T", [3, 150])
+@pytest.mark.parametrize("stage", [0, 2])
+def test_expired_wait_reports_timeout_and_the_device_recovers(T, stage):
+    # one CTA's copy of one stage is never issued and the waits give up after a millisecond
+    blocks = _weights(3, 300, 1600, 31)
+    W = moe.weights_prepare(blocks.cuda(), 3, 300, 1600, wtype="mxfp4")
+    x = torch.randn(T, 1600, generator=torch.Generator().manual_seed(T)).bfloat16().cuda()
+    ids = _ids(T, 2, 3, 32)
+    ws = moe.workspace(T, 2, 3, 1600)
+    moe.lib().moe_testing_stall(0, stage, 1000)
+    try:
+        moe.mul_mat_id_mx4(W, 3, 300, 1600, x, ids.cuda(), ws=ws)
+        st = moe.get_status(ws)
+    finally:
+        moe.lib().moe_testing_stall(-1, 0, 0)
+    assert st == moe.ERR_TIMEOUT
+    site = int(ws[12:16].view(torch.int32).item())  # header word 3
+    assert site >> 30 == 1 and 0 <= (site >> 20) & 0x3ff < 16
+    torch.cuda.synchronize()
+    assert moe.lib().moe_workspace_init(ws.data_ptr(), None) == moe.OK
+    dst = moe.mul_mat_id_mx4(W, 3, 300, 1600, x, ids.cuda(), ws=ws)
+    assert moe.get_status(ws) == moe.OK
+    out, mag = ref.mx_product(blocks.numpy(), x.double().cpu().numpy(), ids.numpy(), False)
+    assert (np.abs(dst.double().cpu().numpy() - out) <= 1600 * 2.0 ** -23 * mag).all()
+
+
+@pytest.mark.parametrize("T", [4, 150])
+def test_a_failed_call_leaves_later_ones_undone_until_the_status_is_read(T):
+    blocks = _weights(4, 32, 64, 41)
+    W = moe.weights_prepare(blocks.cuda(), 4, 32, 64, wtype="mxfp4")
+    x = torch.randn(T, 64, generator=torch.Generator().manual_seed(1)).cuda()
+    ids = _ids(T, 2, 4, 5).cuda()
+    bad = ids.clone()
+    bad[0, 0] = 4
+    ws = moe.workspace(T, 2, 4, 64, x_dtype=torch.float32)
+    out = torch.full((T, 2, 32), -7.0).cuda()
+    moe.mul_mat_id_mx4(W, 4, 32, 64, x, bad, ws=ws, out=out)
+    moe.mul_mat_id_mx4(W, 4, 32, 64, x, ids, ws=ws, out=out)
+    assert moe.get_status(ws) == moe.ERR_BAD_ID
+    assert (out == -7).all()
+    moe.mul_mat_id_mx4(W, 4, 32, 64, x, ids, ws=ws, out=out)
+    assert moe.get_status(ws) == moe.OK and not (out == -7).all()
+
+
+def test_two_calls_at_once_on_two_streams():
+    E, n_out, n_in, k = 8, 384, 1024, 2
+    blocks = _weights(E, n_out, n_in, 43)
+    W = moe.weights_prepare(blocks.cuda(), E, n_out, n_in, wtype="mxfp4")
+    for T in (5, 400):
+        xs = [torch.randn(T, n_in, generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in range(2)]
+        ids = [_ids(T, k, E, 50 + i).cuda() for i in range(2)]
+        want = [moe.mul_mat_id_mx4(W, E, n_out, n_in, xs[i], ids[i]) for i in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        ws = [moe.workspace(T, k, E, n_in) for _ in range(2)]
+        outs = [torch.empty(T, k, n_out).cuda() for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    moe.mul_mat_id_mx4(W, E, n_out, n_in, xs[i], ids[i], ws=ws[i], out=outs[i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 def test_one_expert_takes_all_and_most_take_none():
     blocks = _weights(64, 64, 192, 1)
     x = torch.randn(600, 192, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()

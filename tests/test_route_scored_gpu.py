@@ -78,6 +78,21 @@ def test_keys_closer_than_float32(score):
     _check(l, 8, None, score=score, n_groups=8, topk_groups=3, group_score="top2")
 
 
+def test_group_sums_of_large_opposite_biases():
+    # a group's two largest keys are s + 64 and s' - 64: their sum is a sum of two
+    # scores that a float key cannot hold to better than 2^-18
+    T, G, m = 64, 8, 16
+    g = torch.Generator().manual_seed(4)
+    bias = torch.full((G, m), -1000.0)
+    bias[:, 3], bias[:, 9] = 64.0, -64.0
+    bias = bias.reshape(-1).cuda()
+    l = (torch.randn(T, G * m, generator=g) * 1e-5).cuda()  # sums of scores a few 1e-6 apart
+    for size in (m, 12):  # groups that are whole lanes, and groups that are not
+        E = G * size
+        b, x = bias.view(G, m)[:, :size].reshape(-1).contiguous(), l.view(T, G, m)[:, :, :size].reshape(T, E).contiguous()
+        _check(x, 2, b, n_groups=G, topk_groups=3, group_score="top2")
+
+
 def test_exact_ties_take_the_lower_index():
     l = torch.zeros(3, 96).cuda()
     l[1, 40:] = 1.0
