@@ -2,29 +2,35 @@
 //   dst[t][s] = W[ids[t][s]] . Q(x[t] or x[t][s]),
 // Q rounding every 32 consecutive values to one E8M0 scale and E2M1 codes.
 //
-// Quantising gather: each row is rounded once and its codes go to the tile rows
-// of every slot that reads it: [K plane of 256 values][row][128 bytes], 16-byte
-// chunk c at c ^ (row % 8) (the 128-byte swizzle); the scales of 128 values of
-// a row are one word of [K / 128][row].
+// Rounding: each row is rounded once and its codes go to the tile rows of every
+// slot that reads it: [plane of 256 values][row][128 bytes], the 16-byte chunk
+// of block c at c ^ (row % 8) (the 128-byte swizzle); its scales are two words a
+// plane, [plane][row].
 //
 // Grouped GEMM (tcgen05 kind::mxf4, block scales): a pair of CTAs takes units of
 // (up to 192 sorted rows of one expert) x (two 128-row weight tiles, one a CTA)
-// and streams K in stages of 256 values; a pair MMA reads both CTAs' tiles and
-// half of the rows from each, so that every SM fetches a tile and half the rows
-// for 128 x 192 results - the L2 bytes of a 256 x 192 unit of one CTA - and
+// and streams K in stages of 256 values.  A pair MMA reads both CTAs' tiles and
+// half of the rows from each, so that an SM fetches a tile and half the rows for
+// 128 x 192 results - as little as a 256 x 192 unit of one CTA would - and its
 // tensor memory has room for two accumulators: one is drained while the next
-// fills (one CTA a unit had to stop for the drain, 6000 of 20000 cycles a unit
-// of the skewed 8192-token product).  The 4-bit weights go from their repacked form
-// straight to the tensor cores, no thread touches them.  The codes of a 32-row
-// sub-block are 32 rows of 32 bytes, which the MMA reads in the 32-byte swizzle
-// (address bit 4 ^= bit 7).  Copied as such, in boxes 32 bytes wide, they kept
-// the copy engine busy for ~3.5 cycles a row (567 us for the 4096-token gate
-// product); copied as lines of 128 bytes in the 128-byte swizzle (bits 4-6 ^=
-// bits 7-9) bit 4 comes out the same and bits 5-6 only permute rows: row r of
-// the sub-block lands in row r ^ (r >> 3).  The scales and the epilogue follow
-// that order (perm_row).  Four warps move the scales (1/17 of the
-// bytes) from shared to tensor memory, one thread issues the copies, one the
-// MMAs, and eight warps scatter the accumulators to dst.
+// fills.  (One CTA a unit stopped for the drain, 6000 of 20000 cycles; the GEMM
+// of the 4096-token gate product took 410 us, against 382.)
+//
+// The 4-bit weights go from their repacked form to the tensor cores without
+// passing through threads.  The codes of a 32-row sub-block are 32 rows of 32
+// bytes, which the MMA reads in the 32-byte swizzle (address bit 4 ^= bit 7).
+// Copied as lines of 128 bytes in the 128-byte swizzle (bits 4-6 ^= bits 7-9)
+// bit 4 comes out the same and bits 5-6 only permute rows: row r of the
+// sub-block lands in row r ^ (r >> 3), and the scales and the drain follow that
+// order (perm_row).  (Copied in boxes 32 bytes wide the first kernel took 567 us
+// for that product, in lines 528.)  Four warps move the weights' and the rows'
+// scales from shared to tensor memory, two issue the copies, one thread the
+// MMAs, one warp finds the units, four scatter the accumulators to dst.
+//
+// What bounds it: of the gate product 2.1 GB of weights and 0.27 GB of results
+// (6.2 TB/s at the boost clock, where the copy rate is 6.46; less when the power
+// limit lowers the SM clock); of shapes that reuse the weights from L2 the
+// latency of the stages, 7 in flight, against ~400 cycles of MMAs each.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -46,9 +52,10 @@ bool testing_stall_state(int* cta, int* stage, long long* limit_cycles);
 namespace {
 
 // ----------------------------------------------------------------- geometry
-constexpr int kMxThreads = 512;
+constexpr int kMxThreads = 384;
 constexpr int kMxBN = kGemmBN;    // sorted rows (columns of the accumulator) of a unit
 constexpr int kMxStageKt = 4;     // 64-value k-steps of a stage
+constexpr int kMxDrains = 4;      // warps that drain the accumulators
 constexpr int kMxStages = 7;
 constexpr int kMxScaleSlots = 5;  // stages whose scales have a place in tensor memory
 constexpr uint32_t kMxCodes = kTileM * 32;                 // codes of a tile's k-step
@@ -144,7 +151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     __shared__ int s_prefix[kMxSmemGroups + 1];
     __shared__ int s_bounds[kMxSmemGroups + 1];
     __shared__ int s_pad[kMxSmemGroups + 1];
-    __shared__ __align__(16) int s_rows[8][kMxBN / 2];
+    __shared__ __align__(16) int s_rows[kMxDrains][kMxBN * 4 / kMxDrains];
     __shared__ MxTile s_unit[kMxUnits];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total;
@@ -176,11 +183,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&acc_full[i], 1);
-            ptx::mbar_init(&acc_empty[i], 16);
+            ptx::mbar_init(&acc_empty[i], 2 * kMxDrains);
         }
         for (int i = 0; i < kMxUnits; ++i) {
             ptx::mbar_init(&unit_full[i], 1);
-            ptx::mbar_init(&unit_empty[i], rank == 0 ? 11 : 10);  // two copy warps, eight that drain, the MMAs'
+            ptx::mbar_init(&unit_empty[i], kMxDrains + (rank == 0 ? 3 : 2));  // those that drain, two copy warps, the MMAs'
         }
         ptx::mbar_init(drained, 1);
         s_abort = 0;
@@ -317,8 +324,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         }
     } else if (warp == 1 && rank == 0) {
         // -------------------------------------------------------------- MMAs
-        // One thread's loop: a stage's cycles here are the bound where the clock is low
-        // (the power limit), so the next stage is asked for before this one's MMAs.
+        // One thread's loop (a predicate on each MMA cost ~80 cycles an MMA).  Where the
+        // clock is low, at the power limit, a stage's cycles here are the bound, so the
+        // next stage is asked for before this one's MMAs.
         if (ptx::elect_one()) {
             const uint32_t smem_a = ptx::smem_u32(smem);
             int s = 0, slot = 0;
@@ -404,16 +412,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                 if (++slot == kMxScaleSlots) slot = 0;
             }
         }
-    } else if (warp >= 8 && warp < 16) {
+    } else if (warp >= 8 && warp < 8 + kMxDrains) {
         // ---------------------------------------------------------- epilogue
-        // Four warps (a lane quarter each) drain the first 96 columns, four the rest.
-        const int wq = warp & 3, half = (warp - 8) >> 2;
+        // kMxDrains warps, a lane quarter and a part of the columns each.
+        constexpr int kCols = kMxBN * 4 / kMxDrains;
+        const int wq = warp & 3, part = (warp - 8) >> 2;
         int* rows = s_rows[warp - 8];  // the output rows of the warp's columns
         uint32_t use = 0;
         for (int t = pair; t < total; t += pairs, ++use) {
             MxTile u;
             if (!take_unit((int)use, u)) break;
-            const int mt = u.mu * 2 + (int)rank, c_lo = half * (kMxBN / 2), n = min(kMxBN / 2, u.n - c_lo);
+            const int mt = u.mu * 2 + (int)rank, c_lo = part * kCols, n = min(kCols, u.n - c_lo);
             const uint32_t buf = use & 1;
             __syncwarp();
             for (int c = lane; c < n; c += 32) rows[c] = __ldg(p.dst_rows + u.p0 + c_lo + c);
@@ -425,7 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
             float* out = p.out + m;
             // A column is a sorted row: its 32 lanes are 128 consecutive bytes of one
             // row of dst.  The rows' numbers come from shared memory, four to a load: by
-            // shuffles under a test a column cost 105 cycles against ~25.
+            // shuffles under a test a column cost 105 cycles.
             for (int c0 = 0; c0 < n; c0 += 32) {
                 uint32_t v[32];
                 ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + buf * kMxBN + c_lo + c0, v);
@@ -602,18 +611,20 @@ mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restric
 }
 
 // ------------------------------------------- row ids and gather in two launches
-// For up to kRidMaxE experts the tables come from two launches instead of the
-// row-id pass and a gather (35 + 60 us of a 4096-token gate product, 32 + 98 us
-// of the skewed 8192-token one): one counts the slots of each chunk of tokens by
-// expert; in the other each CTA, one of kMpParts of a chunk, sums the counts
-// before its own (the place of its first slot of every expert, the tables'
-// prefixes), ranks its slots in slot order - the same stable counting sort -
-// and rounds its rows straight into their tile rows.  The second launch starts
-// while the first runs, with the count of its chunk's slots before its own.
-// (With a count for every CTA, all of them reading 148 counts an expert took
-// 6.7 us.)
+// For up to kRidMaxE experts one launch of up to 148 CTAs makes the tables and
+// gathers, instead of the row-id pass and a gather (35 + 60 us of a 4096-token
+// gate product, 32 + 98 us of the skewed 8192-token one).  Each CTA counts the
+// slots by expert before its own and in all (the place of its first slot of
+// every expert, the tables' prefixes), ranks its slots in slot order - the same
+// stable counting sort - and rounds its rows straight into their tile rows.
+// Up to kMpSelfSlots slots every CTA reads all the ids.  Beyond, a launch before
+// counts the chunk of kMpParts CTAs and a CTA sums the chunks' counts and counts
+// its chunk's slots before its own, while that launch runs.  (The whole call
+// for 512 slots, 256 experts, 2048 -> 512: 42 us by itself, 46 with the launch
+// before; at 32768 slots there is no difference.)
 constexpr int kMpThreads = 1024;
 constexpr int kMpMaxCtas = 148, kMpParts = 4;
+constexpr int64_t kMpSelfSlots = 32768;
 static_assert((kMpMaxCtas + kMpParts - 1) / kMpParts <= 2 * kRidMaxCtas, "counts take the row-id pass's scratch");
 
 __device__ __forceinline__ int64_t mp_token(int64_t T, int g, int G) { return T * g / G; }
@@ -622,10 +633,16 @@ __device__ __forceinline__ int64_t mp_token(int64_t T, int g, int G) { return T 
 // matter).  An id outside [0, E) is left out; true where one was met.
 __device__ __forceinline__ bool count_slots(const int32_t* __restrict__ ids, int s0, int s1, int E, int* cnt) {
     bool bad = false;
-    for (int i = s0 + threadIdx.x; i < s1; i += kMpThreads) {
-        const int e = __ldg(ids + i);
-        if ((unsigned)e < (unsigned)E) atomicAdd(&cnt[e], 1);
-        else bad = true;
+    for (int i0 = s0 + threadIdx.x; i0 < s1; i0 += 8 * kMpThreads) {  // eight loads in flight
+        int e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = s1 - i0 > j * kMpThreads ? __ldg(ids + i0 + j * kMpThreads) : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (s1 - i0 <= j * kMpThreads) break;
+            if ((unsigned)e[j] < (unsigned)E) atomicAdd(&cnt[e[j]], 1);
+            else bad = true;
+        }
     }
     return bad;
 }
@@ -686,31 +703,32 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t t0 = mp_token(p.T, g, G), t1 = mp_token(p.T, g + 1, G);
     const int64_t r0 = p.per_slot ? t0 * k : t0, r1 = p.per_slot ? t1 * k : t1;
-    for (int e = tid; e < E; e += kMpThreads) s_base[e] = 0;
+    // counts before this CTA's slots (or, here, those of its chunk) and in all
+    int before = 0, all = 0;
+    for (int e = tid; e < E; e += kMpThreads) s_base[e] = s_row[e] = 0;
     __syncthreads();
-    const int chunk = g / kMpParts, C = (G + kMpParts - 1) / kMpParts;
-    count_slots(p.ids, (int)(mp_token(p.T, chunk * kMpParts, G) * k), (int)(t0 * k), E, s_base);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (read_status(p.hdr + kHdrStatus) != 0) return;
-    // counts before this CTA's and in all: 1024 / E threads an expert, each some of the rows
-    const int Ep = (E + 31) & ~31, parts = kMpThreads / Ep;
-    {
-        int before = 0, all = 0;
+    if (!p.counts) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const bool stop = tid == 0 && read_status(p.hdr + kHdrStatus) != 0;
+        bool bad = count_slots(p.ids, 0, (int)(t0 * k), E, s_base);
+        bad |= count_slots(p.ids, (int)(t0 * k), (int)(p.T * k), E, s_row);
+        if (bad) set_status(p.hdr + kHdrStatus, MOE_ERR_BAD_ID);
+        if (__syncthreads_or(bad || stop)) return;
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (tid < E) all = s_base[tid] + s_row[tid];
+        __syncthreads();
+    } else {
+        const int chunk = g / kMpParts, C = (G + kMpParts - 1) / kMpParts;
+        count_slots(p.ids, (int)(mp_token(p.T, chunk * kMpParts, G) * k), (int)(t0 * k), E, s_base);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (__syncthreads_or(tid == 0 && read_status(p.hdr + kHdrStatus) != 0)) return;
+        // 1024 / E threads an expert, each some of the chunks
+        const int Ep = (E + 31) & ~31, parts = kMpThreads / Ep;
         const int e = tid % Ep, part = tid / Ep;
         if (part < parts && e < E) {
-            int c = part;
-            for (; c + 7 * parts < C; c += 8 * parts) {
-                int v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __ldcg(p.counts + (size_t)(c + i * parts) * E + e);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    all += v[i];
-                    before += c + i * parts < chunk ? v[i] : 0;
-                }
-            }
-            for (; c < C; c += parts) {
+#pragma unroll 8
+            for (int c = part; c < C; c += parts) {
                 const int v = __ldcg(p.counts + (size_t)c * E + e);
                 all += v;
                 before += c < chunk ? v : 0;
@@ -721,15 +739,15 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
             s_row[part * 2 * Ep + e] = before;
             s_row[(part * 2 + 1) * Ep + e] = all;
         }
-    }
-    __syncthreads();
-    {
-        int before = 0, all = 0;
+        __syncthreads();
+        before = all = 0;
         if (tid < E)
             for (int i = 0; i < parts; ++i) {
                 before += s_row[i * 2 * Ep + tid];
                 all += s_row[(i * 2 + 1) * Ep + tid];
             }
+    }
+    {
         int S, tiles, padded;
         const int b = cta_prefix(all, s_sums, &S);
         const int q = cta_prefix((all + kMxBN - 1) / kMxBN, s_sums, &tiles);
@@ -812,7 +830,7 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
 // accumulator.
 constexpr int kMdThreads = 384;
 constexpr int kMdRounders = 6;      // warps 2, 3, 8-11
-constexpr int kMdMaxSlots = 256;
+constexpr int kMdMaxSlots = 128;
 constexpr int kMdN = 16;            // columns of an accumulator
 constexpr int kMdMaxPlanes = 36;    // K up to 9216
 constexpr int kMdKt = 8;            // k-steps of a stage: half the copies to issue, ~450 cycles a stage
@@ -820,12 +838,9 @@ constexpr int kMdMaxStages = 5;
 constexpr uint32_t kMdCodes = kMdKt * kMxCodes, kMdScales = kMdKt * 256, kMdStage = kMdCodes + kMdScales;
 constexpr uint32_t kMdPlane = kMdN * 128, kMdPlaneScales = 2 * kMdN * 4;
 constexpr uint32_t kMdSmem = 211 * 1024;
-// Tensor memory: two times four accumulators (MMAs into one accumulator wait for
-// one another; k-step j of a stage goes to accumulator j % 4 and the drain adds
-// the four), the stages' A scales (16 columns each), the B scales of all of K (4 columns per 128 values, 16 rows take the
-// first).
-constexpr uint32_t kMdAcc = 4 * kMdN;
-constexpr uint32_t kMdColA = 2 * kMdAcc, kMdColB = kMdColA + 2 * kMdKt * kMdMaxStages;
+// Tensor memory: two accumulators, the stages' A scales (16 columns each), the B
+// scales of all of K (4 columns per 128 values, of which 16 rows take the first).
+constexpr uint32_t kMdColA = 2 * kMdN, kMdColB = kMdColA + 2 * kMdKt * kMdMaxStages;
 static_assert(kMdColA % 4 == 0 && kMdColB % 4 == 0 && kMdColB + 8 * kMdMaxPlanes <= 512, "tensor memory");
 constexpr int kMdBarRed = 1;  // named barrier of the workers
 
@@ -1039,9 +1054,9 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                 const int kts = KT - ks * kMdKt;
                 if (issue) {
                     auto step = [&](int j) {
-                        ptx::mma_mxf4_ss(tmem + buf * kMdAcc + (j & 3) * kMdN, ad + (j * kMxCodes >> 4),
+                        ptx::mma_mxf4_ss(tmem + buf * kMdN, ad + (j * kMxCodes >> 4),
                                          bd + ((j >> 2) * kMdPlane >> 4) + (j & 3) * 2, j & 1 ? id1 : id0,
-                                         sfa + (j >> 1) * 4, sfb + (j >> 1) * 4, ks != 0 || j > 3);
+                                         sfa + (j >> 1) * 4, sfb + (j >> 1) * 4, (ks | j) != 0);
                     };
                     if (kts >= kMdKt) {
 #pragma unroll
@@ -1156,25 +1171,19 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
             uint32_t slots[kMdN / 2];  // two a word
 #pragma unroll
             for (int j = 0; j < kMdN / 2; ++j) slots[j] = ((const uint32_t*)s_slots[g])[j];
-            const int m = mt * kTileM + 32 * (warp & 3) + perm_row(lane), parts = min(KT, 4);
+            const int m = mt * kTileM + 32 * (warp & 3) + perm_row(lane);
             ok = ok && warp_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, status, p.wait_limit);
             if (ok) {
                 ptx::tc_fence_after();
-                uint32_t v[4][kMdN];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < parts) ptx::tmem_ld_32x32b_x16(lanes + buf * kMdAcc + i * kMdN, v[i]);
+                uint32_t v[kMdN];
+                ptx::tmem_ld_32x32b_x16(lanes + buf * kMdN, v);
                 ptx::tmem_ld_wait();
                 if (m < L.n_out) {
 #pragma unroll
-                    for (int j = 0; j < kMdN; ++j) {
-                        if (j >= rows) break;
-                        float r = __uint_as_float(v[0][j]);
-#pragma unroll
-                        for (int i = 1; i < 4; ++i)
-                            if (i < parts) r = __fadd_rn(r, __uint_as_float(v[i][j]));
-                        p.out[(int64_t)(slots[j / 2] >> (16 * (j & 1)) & 0xffffu) * p.out_ld + m] = r;
-                    }
+                    for (int j = 0; j < kMdN; ++j)
+                        if (j < rows)
+                            p.out[(int64_t)(slots[j / 2] >> (16 * (j & 1)) & 0xffffu) * p.out_ld + m] =
+                                __uint_as_float(v[j]);
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -1348,7 +1357,12 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     p.W = (const uint8_t*)W_prepared;
     p.L = WLayout(n_out, n_in, MOE_MXFP4);
     const int planes = (n_in + 255) / 256;
-    const bool few = S <= kMdMaxSlots && planes <= kMdMaxPlanes;
+    // One launch for few slots, unless they crowd on few experts (a group holds kMdN
+    // slots and streams its expert's weights again).  256 experts, top-8, 2048 -> 512,
+    // one launch / two: 14 / 21 us at 32 slots, 25 / 30 at 128, 35 / 38 at 256;
+    // 7168 -> 2048: 96 / 103 at 64, 217 / 213 at 256; 8 experts, top-8, 4096 -> 4096:
+    // 67 / 32 at 256.
+    const bool few = S <= kMdMaxSlots && S <= (int64_t)kMdN * n_experts && planes <= kMdMaxPlanes;
     if (!plan_weights(p, n_experts, few ? kMdKt : kMxStageKt)) return MOE_ERR_CUDA;
     p.out = dst;
     p.out_ld = n_out;
@@ -1389,11 +1403,13 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     moe_status st;
     if (n_experts <= kRidMaxE) {
         const unsigned G = (unsigned)(n_tokens < kMpMaxCtas ? n_tokens : kMpMaxCtas);
-        int32_t* counts = (int32_t*)(ws + W.rid);
-        mx4_count_kernel<<<(G + kMpParts - 1) / kMpParts, kMpThreads, (size_t)n_experts * sizeof(int), s>>>(
-            ids, n_tokens, k, n_experts, (int)G, counts, hdr);
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-        prof_mark(s, "row_ids");
+        int32_t* counts = S > kMpSelfSlots ? (int32_t*)(ws + W.rid) : nullptr;
+        if (counts) {
+            mx4_count_kernel<<<(G + kMpParts - 1) / kMpParts, kMpThreads, (size_t)n_experts * sizeof(int), s>>>(
+                ids, n_tokens, k, n_experts, (int)G, counts, hdr);
+            if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+            prof_mark(s, "row_ids");
+        }
         MxPlaceArgs a = {ids, x, n_in, n_tokens, k, n_experts, !broadcast, counts, (int32_t*)(ws + W.bounds),
                          (int32_t*)(ws + W.tiles), (int32_t*)(ws + W.pad), (int32_t*)(ws + W.dst),
                          (int32_t*)(ws + W.sprow), hdr, o};

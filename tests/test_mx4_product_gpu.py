@@ -84,6 +84,13 @@ def test_many_experts(T, E, k):
     _check(blocks, x, _ids(T, k, E, T), "broadcast")
 
 
+@pytest.mark.parametrize("mode,T,k", [("broadcast", 11000, 3), ("per_slot", 16400, 2)])
+def test_more_slots_than_a_cta_counts(mode, T, k):
+    blocks = _weights(7, 17, 64, T)
+    x = torch.randn(T if mode == "broadcast" else T * k, 64, generator=torch.Generator().manual_seed(T)).bfloat16().cuda()
+    _check(blocks, x, _ids(T, k, 7, T), mode)
+
+
 @pytest.mark.parametrize("T,n_in", [(2, 9216), (2, 9248), (1, 12320)])
 def test_long_rows(T, n_in):
     # the longest that the one-launch form holds in shared memory, and past it
