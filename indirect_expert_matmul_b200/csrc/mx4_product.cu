@@ -65,8 +65,10 @@ constexpr uint32_t kMxB = kMxBN / 2 * 128;                 // 12288: half the ro
 constexpr uint32_t kMxBScales = kMxBN * 8;                 // 1536: every row's two words
 constexpr uint32_t kMxOffB = kMxACodes, kMxOffAS = kMxOffB + kMxB, kMxOffBS = kMxOffAS + kMxAScales;
 constexpr uint32_t kMxStagePitch = (kMxOffBS + kMxBScales + 1023) / 1024 * 1024;
+constexpr int kMxUnits = 2;       // units known ahead
 constexpr uint32_t kMxBarOff = kMxStages * kMxStagePitch;
-constexpr uint32_t kMxSmem = kMxBarOff + 256 + 1024;
+constexpr uint32_t kMxBars = 3 * kMxStages + 4 + 4 * kMxUnits + 1;
+constexpr uint32_t kMxSmem = kMxBarOff + kMxBars * 8 + 1024;
 // tensor memory: two accumulators, then per slot 8 columns of A scales (two
 // 128-value halves x four) and 16 of B scales (two halves x eight)
 constexpr uint32_t kMxScaleCol0 = 2 * kMxBN, kMxScaleCols = 24;
@@ -144,7 +146,6 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, 
 struct MxTile {
     int e, mu, p0, n, p0pad;
 };
-constexpr int kMxUnits = 4;  // units known ahead
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_gemm_kernel(const __grid_constant__ Mx4Params p) {
     extern __shared__ uint8_t smem_dyn[];
@@ -152,7 +153,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     __shared__ int s_bounds[kMxSmemGroups + 1];
     __shared__ int s_pad[kMxSmemGroups + 1];
     __shared__ __align__(16) int s_rows[kMxDrains][kMxBN * 4 / kMxDrains];
-    __shared__ MxTile s_unit[kMxUnits];
+    __shared__ MxTile s_unit[kMxUnits];  // n == 0: no more
+    __shared__ int s_next[2 * kMxUnits];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total;
 
@@ -164,7 +166,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     uint64_t* acc_empty = acc_full + 2;              // [2]
     uint64_t* unit_full = acc_empty + 2;             // [kMxUnits]
     uint64_t* unit_empty = unit_full + kMxUnits;     // [kMxUnits]
-    uint64_t* drained = unit_empty + kMxUnits;
+    uint64_t* next_full = unit_empty + kMxUnits;     // [2 * kMxUnits], of CTA 1
+    uint64_t* drained = next_full + 2 * kMxUnits;
     volatile int* abort_flag = &s_abort;
     int* status = p.hdr + kHdrStatus;
 
@@ -187,8 +190,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         }
         for (int i = 0; i < kMxUnits; ++i) {
             ptx::mbar_init(&unit_full[i], 1);
-            ptx::mbar_init(&unit_empty[i], kMxDrains + (rank == 0 ? 3 : 2));  // those that drain, two copy warps, the MMAs'
+            ptx::mbar_init(&unit_empty[i], 4 + kMxDrains + (rank == 0 ? 3 : 2));  // scales, drains, two copy warps, the MMAs'
         }
+        for (int i = 0; i < 2 * kMxUnits; ++i) ptx::mbar_init(&next_full[i], 1);
         ptx::mbar_init(drained, 1);
         s_abort = 0;
         ptx::fence_mbar_init();
@@ -203,17 +207,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     const uint32_t tmem = uniform(s_tmem);
     // (a programmatic dependent of the rounding: nothing it wrote is read before it has ended)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // (all threads by one thread's reading: another CTA may set the status meanwhile)
+    // (by one thread's reading: another CTA may set the status meanwhile; CTA 1 goes by CTA 0's units)
     if (tid == 0) s_total = read_status(status) != 0 ? 0 : p.hdr[kHdrTiles] * MU;
-    __syncthreads();
-    const int total = uniform(s_total);
-    if (in_smem && total > 0)
+    if (in_smem)
         for (int i = tid; i <= p.n_groups; i += kMxThreads) {
             s_prefix[i] = p.ntile_prefix[i];
             s_bounds[i] = p.bounds[i];
             s_pad[i] = p.pad_start[i];
         }
     __syncthreads();
+    const int total = uniform(s_total);
 
     // Unit t, by a whole warp: the largest group whose first column tile is at most
     // q, 32 candidates a step (by bisection a unit's start cost ~1000 cycles).
@@ -237,16 +240,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         return r;
     };
 
-    // Units are found by warp 3, up to kMxUnits ahead; the others take them from
-    // shared memory (found by each role itself, a unit's start was a gap of 2500
-    // cycles in the MMAs).
+    // Units are found by warp 3, ahead; the others take them from shared memory
+    // (found by each role itself, a unit's start was a gap of 2500 cycles in the
+    // MMAs).  False behind the last, or where a wait has expired.
     auto take_unit = [&](int k, MxTile& u) {
         const int slot = k % kMxUnits;
         if (!warp_wait(&unit_full[slot], (uint32_t)(k / kMxUnits) & 1u, abort_flag, status, p.wait_limit)) return false;
         u = s_unit[slot];
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&unit_empty[slot]);
-        return true;
+        return u.n > 0;
     };
 
     if (warp == 0) {
@@ -255,10 +258,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         int s = 0;
         uint32_t ph = 0, used = 0, par = 0;
         bool ok = true;
-        for (int t = pair, k = 0; t < total && ok; t += pairs, ++k) {
-            MxTile u;
-            ok = take_unit(k, u);
-            if (!ok) break;
+        MxTile u;
+        for (int k = 0; ok && take_unit(k, u); ++k) {
             const int mt = u.mu * 2 + (int)rank;
             for (int ks = 0; ks < KS; ++ks) {
                 ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
@@ -286,10 +287,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         int s = 0, q = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int t = pair, k = 0; t < total && ok; t += pairs, ++k) {
-            MxTile u;
-            ok = take_unit(k, u);
-            if (!ok) break;
+        MxTile u;
+        for (int k = 0; ok && take_unit(k, u); ++k) {
             const uint32_t nh = (uint32_t)(u.n + 31) / 32u * 16u;
             const uint8_t* bsrc = p.B + (size_t)(u.p0pad + (int)(rank * nh)) * 128u;
             const uint2* ssrc = p.BS + u.p0pad;
@@ -310,17 +309,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         }
     } else if (warp == 3) {
         // -------------------------------------------------------------- units
+        // A pair's first unit goes by its number, every further one is the next that no
+        // pair has (units differ in their rows; by number alone the pairs of the skewed
+        // 8192-token product idled for 10 % of the launch).  CTA 0 asks and tells CTA 1,
+        // in a ring that needs no answer: that a slot of s_unit is free again says that
+        // the MMAs of unit k - kMxUnits have begun, so those of the unit before it were
+        // all issued, for which CTA 1 had read that unit's number, and k - 2 * kMxUnits
+        // is no later.
+        static_assert(kMxUnits >= 1, "the ring of numbers is read in time");
         bool ok = true;
-        for (int t = pair, k = 0; t < total && ok; t += pairs, ++k) {
-            const int slot = k % kMxUnits;
-            const MxTile u = unit(t);
+        int ahead = 0;
+        for (int k = 0; ok; ++k) {
+            const int slot = k % kMxUnits, n = k % (2 * kMxUnits);
+            int t = pair;
+            if (rank == 0) {
+                if (k > 0) t = ahead;
+                if (t >= total) t = -1;
+                if (t >= 0) {
+                    if (lane == 0) ahead = pairs + atomicAdd(p.hdr + kHdrUnits, 1);
+                    ahead = uniform(ahead);
+                }
+            }
             ok = warp_wait(&unit_empty[slot], ((uint32_t)(k / kMxUnits) & 1u) ^ 1u, abort_flag, status, p.wait_limit);
             if (!ok) break;
+            if (rank == 0) {
+                if (lane == 0) {
+                    ptx::st_cluster(&s_next[n], 1, (uint32_t)t);
+                    ptx::mbar_arrive_cluster<true>(&next_full[n], 1);
+                }
+                __syncwarp();
+            } else {
+                ok = warp_wait<true>(&next_full[n], (uint32_t)(k / (2 * kMxUnits)) & 1u, abort_flag, status, p.wait_limit);
+                if (!ok) break;
+                t = *(volatile int*)&s_next[n];
+            }
+            MxTile u = {};
+            if (t >= 0) u = unit(t);
             if (lane == 0) {
                 s_unit[slot] = u;
                 ptx::mbar_arrive(&unit_full[slot]);
             }
             __syncwarp();
+            if (t < 0) break;
         }
     } else if (warp == 1 && rank == 0) {
         // -------------------------------------------------------------- MMAs
@@ -332,12 +362,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
             int s = 0, slot = 0;
             uint32_t ph = 0, use = 0;
             bool ok = true, ready = false;
-            for (int t = pair; t < total && ok; t += pairs, ++use) {
+            for (; ok; ++use) {
                 const int k = (int)use % kMxUnits;
                 ok = wait_bar(&unit_full[k], (use / kMxUnits) & 1u, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 const int n32 = (s_unit[k].n + 31) & ~31;
                 ptx::mbar_arrive(&unit_empty[k]);
+                if (n32 == 0) break;
                 const uint32_t id0 = ptx::idesc_mxf4(n32, 0, 256), id1 = ptx::idesc_mxf4(n32, 1, 256), buf = use & 1;
                 const uint32_t d = tmem + buf * kMxBN;
                 ok = wait_bar<true>(&acc_empty[buf], ((use >> 1) & 1) ^ 1, abort_flag, status, p.wait_limit);
@@ -385,7 +416,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         uint32_t ph = 0, old_ph = 0;
         bool ok = true;
         const uint32_t dst = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + kMxScaleCol0;
-        for (int t = pair; t < total && ok; t += pairs) {
+        MxTile u;
+        for (int k = 0; ok && take_unit(k, u); ++k) {
             for (int ks = 0; ks < KS; ++ks) {
                 ok = warp_wait(&full[s], ph, abort_flag, status, p.wait_limit) &&
                      (old < 0 || warp_wait(&empty[old], old_ph, abort_flag, status, p.wait_limit));
@@ -419,9 +451,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         const int wq = warp & 3, part = (warp - 8) >> 2;
         int* rows = s_rows[warp - 8];  // the output rows of the warp's columns
         uint32_t use = 0;
-        for (int t = pair; t < total; t += pairs, ++use) {
-            MxTile u;
-            if (!take_unit((int)use, u)) break;
+        MxTile u;
+        for (; take_unit((int)use, u); ++use) {
             const int mt = u.mu * 2 + (int)rank, c_lo = part * kCols, n = min(kCols, u.n - c_lo);
             const uint32_t buf = use & 1;
             __syncwarp();
@@ -600,8 +631,9 @@ __device__ __forceinline__ void round_planes(const void* __restrict__ x, int64_t
 template <int TYPE>
 __global__ void __launch_bounds__(256)
 mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restrict__ slot_prow, int copies,
-                  int64_t n_rows, MxRows o, const int* hdr) {
+                  int64_t n_rows, MxRows o, int* hdr) {
     if (read_status(hdr + kHdrStatus) != 0) return;
+    if (blockIdx.x == 0 && threadIdx.x == 0) hdr[kHdrUnits] = 0;
     const int lane = threadIdx.x & 31;
     const int planes = (n_in + 255) / 256;
     const int64_t nw = (int64_t)gridDim.x * (blockDim.x / 32);
@@ -766,6 +798,7 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
             p.ntile_prefix[E] = tiles;
             p.pad_start[E] = padded;
             p.hdr[kHdrTiles] = tiles;
+            p.hdr[kHdrUnits] = 0;
         }
     }
     __syncthreads();

@@ -68,6 +68,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank
             "r"(rank)
             : "memory");
 }
+// A word of the cluster's CTA `rank`, at this CTA's address.
+__device__ __forceinline__ void st_cluster(int* p, uint32_t rank, uint32_t v) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(smem_u32(p)),
+        "r"(rank), "r"(v)
+        : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
