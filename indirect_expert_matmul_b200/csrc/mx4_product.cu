@@ -354,14 +354,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         }
     } else if (warp == 1 && rank == 0) {
         // -------------------------------------------------------------- MMAs
-        // One thread's loop (a predicate on each MMA cost ~80 cycles an MMA).  Where the
-        // clock is low, at the power limit, a stage's cycles here are the bound, so the
-        // next stage is asked for before this one's MMAs.
+        // One thread's loop (a predicate on each MMA cost ~80 cycles an MMA).
         if (ptx::elect_one()) {
             const uint32_t smem_a = ptx::smem_u32(smem);
             int s = 0, slot = 0;
             uint32_t ph = 0, use = 0;
-            bool ok = true, ready = false;
+            bool ok = true;
             for (; ok; ++use) {
                 const int k = (int)use % kMxUnits;
                 ok = wait_bar(&unit_full[k], (use / kMxUnits) & 1u, abort_flag, status, p.wait_limit);
@@ -375,17 +373,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                 if (!ok) break;
                 for (int ks = 0; ks < KS; ++ks) {
                     // (the scale warps of both CTAs arrive after they have seen the stage's copies land)
-                    ok = ready || wait_bar<true>(&sf_full[s], ph, abort_flag, status, p.wait_limit);
+                    ok = wait_bar<true>(&sf_full[s], ph, abort_flag, status, p.wait_limit);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t st = smem_a + (uint32_t)s * kMxStagePitch;
                     const uint32_t sf = tmem + kMxScaleCol0 + (uint32_t)slot * kMxScaleCols;
                     const uint64_t ad = ptx::desc_k_sw32(st), bd = ptx::desc_k_sw128(st + kMxOffB);
                     const int kts = KT - ks * kMxStageKt;
-                    uint64_t* done = &empty[s];
-                    if (++s == kMxStages) { s = 0; ph ^= 1; }
-                    if (++slot == kMxScaleSlots) slot = 0;
-                    ready = ptx::mbar_try_wait_cluster(&sf_full[s], ph);
                     auto step = [&](int j) {  // address fields count 16 bytes; sums stay inside their 14 bits
                         ptx::mma_mxf4_pair(d, ad + (j * kMxCodes >> 4), bd + j * 2, j & 1 ? id1 : id0, sf + (j >> 1) * 4,
                                            sf + 8 + (j >> 1) * 8, (ks | j) != 0);
@@ -396,7 +390,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                     } else {
                         for (int j = 0; j < kts; ++j) step(j);
                     }
-                    ptx::mma_commit_pair(done);
+                    ptx::mma_commit_pair(&empty[s]);
+                    if (++s == kMxStages) { s = 0; ph ^= 1; }
+                    if (++slot == kMxScaleSlots) slot = 0;
                 }
                 if (!ok) break;
                 ptx::mma_commit_pair(&acc_full[buf]);
