@@ -32,6 +32,7 @@ namespace {
 constexpr int kRsWarps = 4;
 constexpr int kRsMaxPerLane = 32;  // n_experts <= 1024
 constexpr int kRsMaxGroups = 32;
+constexpr int64_t kRsHalfTokens = 148 * 32;  // above: a scheduler has more than 8 tokens
 
 __device__ __forceinline__ float load_logit(const void* p, int type, int64_t i) {
     if (type == MOE_F32) return __ldg((const float*)p + i);
@@ -39,16 +40,21 @@ __device__ __forceinline__ float load_logit(const void* p, int type, int64_t i) 
     return type == MOE_BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// Over the LANES lanes of `mask` (a token's), in a fixed order.
+template <int LANES>
+__device__ __forceinline__ float group_max(float v, uint32_t mask) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
     return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v, uint32_t mask) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(mask, v, o));
     return v;
 }
+__device__ __forceinline__ float warp_max(float v) { return group_max<32>(v, 0xffffffffu); }
+__device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v, 0xffffffffu); }
 
 // sigmoid(l) * exp(-c) for c <= 0, c >= min(l, 0): no overflow, and no underflow for l near c.
 __device__ __forceinline__ float sigmoid_over(float l, float c) {
@@ -569,24 +575,26 @@ __device__ __forceinline__ void store_row(void* base, int type, int64_t first, i
 //   sigmoid:              dl[ids_i] += g_i s_i (1 - s_i)
 //   softmax, normalised:  dl[ids_i] += p_i (g_i - sum_j g_j p_j)
 //   softmax:              dl[e]      = s_e (sum of g_i with ids_i = e  -  sum_j g_j s_{ids_j})
-// One warp per token.  The slots' terms go to the row's place in shared memory
+// LANES lanes a token.  The slots' terms go to the row's place in shared memory
 // and come back NPL consecutive experts a lane, so that the row is written with
 // wide stores; only the last form reads the whole row of logits.  A slot whose
 // id is outside [0, n_experts) is left out.
-template <int NPL>
+template <int NPL, int LANES>
 __global__ void __launch_bounds__(kRsWarps * 32) route_scored_bwd_kernel(const RouteScoredBwdArgs p) {
-    __shared__ __align__(16) float s_rows[kRsWarps][32 * NPL];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * kRsWarps + warp;
+    constexpr int kRows = kRsWarps * 32 / LANES;
+    __shared__ __align__(16) float s_rows[kRows][LANES * NPL];
+    const int lane = threadIdx.x % LANES, place = threadIdx.x / LANES;
+    const uint32_t mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
+    const int64_t t = (int64_t)blockIdx.x * kRows + place;
     if (t >= p.n_tokens) return;
     const int E = p.n_experts, e0 = lane * NPL;
     const int32_t* it = p.ids + t * p.k;
     const float* gt = p.dw + t * p.k;
-    float* row = s_rows[warp];
+    float* row = s_rows[place];
     const bool dense = p.softmax && !p.normalize;
     float l[NPL];
     if (dense) load_row<NPL>(p.logits, p.type, t * p.ld, E, lane, p.vec & 1, -INFINITY, l);
-    // the first 32 slots stay in registers
+    // the first LANES slots stay in registers
     auto slot_id = [&](int i) {
         const int e = it[i];
         return (unsigned)e < (unsigned)E ? e : -1;
@@ -596,15 +604,15 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_bwd_kernel(const R
     const float g0 = lane < p.k ? __ldg(gt + lane) : 0.f;
     const float l0 = slot_logit(id0);
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) row[j * 32 + lane] = 0.f;
+    for (int j = 0; j < NPL; ++j) row[j * LANES + lane] = 0.f;
     float top = l0;
     if (dense) {
 #pragma unroll
         for (int j = 0; j < NPL; ++j) top = fmaxf(top, l[j]);
     } else {
-        for (int i = 32 + lane; i < p.k; i += 32) top = fmaxf(top, slot_logit(slot_id(i)));
+        for (int i = LANES + lane; i < p.k; i += LANES) top = fmaxf(top, slot_logit(slot_id(i)));
     }
-    top = warp_max(top);
+    top = group_max<LANES>(top, mask);
     const float c = p.softmax ? top : p.normalize ? fminf(top, 0.f) : 0.f;
     const bool dead = c == -INFINITY;
     auto raw = [&](float v) {  // the score over the common factor
@@ -619,21 +627,21 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_bwd_kernel(const R
         }
     }
     const float r0 = raw(l0);
-    for (int i = lane; i < p.k; i += 32) {
-        const float r = i < 32 ? r0 : raw(slot_logit(slot_id(i)));
+    for (int i = lane; i < p.k; i += LANES) {
+        const float r = i < LANES ? r0 : raw(slot_logit(slot_id(i)));
         if (!dense) z = __fadd_rn(z, r);
-        dot = __fmaf_rn(i < 32 ? g0 : gt[i], r, dot);
+        dot = __fmaf_rn(i < LANES ? g0 : gt[i], r, dot);
     }
     if (!p.normalize && !p.softmax) {
         z = 1.f;
         dot = 0.f;
     } else {
-        z = warp_sum(z);
-        dot = warp_sum(dot);
+        z = group_sum<LANES>(z, mask);
+        dot = group_sum<LANES>(dot, mask);
         dot = dead ? 0.f : __fdiv_rn(dot, z);
     }
-    __syncwarp();
-    for (int i0 = 0; i0 < p.k; i0 += 32) {
+    __syncwarp(mask);
+    for (int i0 = 0; i0 < p.k; i0 += LANES) {
         const int i = i0 + lane;
         int e = id0;
         float v = 0.f;
@@ -654,16 +662,16 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_bwd_kernel(const R
         } else {
             e = -1;
         }
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (__all_sync(0xffffffffu, e < 0 || (same & (same - 1)) == 0u)) {
+        const uint32_t same = __match_any_sync(mask, e);
+        if (__all_sync(mask, e < 0 || (same & (same - 1)) == 0u)) {
             if (e >= 0) row[e] = __fadd_rn(row[e], v);
         } else {
-            for (int q = 0; q < 32; ++q) {  // an id occurs twice: in slot order, the same way each time
+            for (int q = 0; q < LANES; ++q) {  // an id occurs twice: in slot order, the same way each time
                 if (lane == q && e >= 0) row[e] = __fadd_rn(row[e], v);
-                __syncwarp();
+                __syncwarp(mask);
             }
         }
-        __syncwarp();
+        __syncwarp(mask);
     }
     float v[NPL];
     if constexpr (NPL % 4 == 0) {
@@ -685,10 +693,11 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_bwd_kernel(const R
     store_row<NPL>(p.out, p.type, t * E, E, lane, p.vec & 2, v);
 }
 
-template <int NPL>
+template <int NPL, int LANES>
 void launch_bwd(const RouteScoredBwdArgs& a, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((a.n_tokens + kRsWarps - 1) / kRsWarps);
-    route_scored_bwd_kernel<NPL><<<blocks, kRsWarps * 32, 0, s>>>(a);
+    constexpr int kRows = kRsWarps * 32 / LANES;
+    const unsigned blocks = (unsigned)((a.n_tokens + kRows - 1) / kRows);
+    route_scored_bwd_kernel<NPL, LANES><<<blocks, kRsWarps * 32, 0, s>>>(a);
 }
 
 bool valid_dtype(int t) { return t == MOE_BF16 || t == MOE_F16 || t == MOE_F32; }
@@ -750,11 +759,19 @@ extern "C" moe_status moe_route_scored_backward(const void* logits, moe_dtype l_
                             (rows_aligned(logits, l_type, row_stride) ? 1 : 0) |
                                 (rows_aligned(dlogits, l_type, n_experts) ? 2 : 0)};
     cudaStream_t s = (cudaStream_t)stream;
-    if (n_experts <= 32) launch_bwd<1>(a, s);
-    else if (n_experts <= 64) launch_bwd<2>(a, s);
-    else if (n_experts <= 128) launch_bwd<4>(a, s);
-    else if (n_experts <= 256) launch_bwd<8>(a, s);
-    else if (n_experts <= 512) launch_bwd<16>(a, s);
-    else launch_bwd<32>(a, s);
+    // Half a warp a token where that leaves fewer instructions and there are enough
+    // tokens to hide its longer chain: 128 experts, softmax, 16 / 32 lanes, us:
+    // 3.5 / 3.2 at 4096 tokens, 3.8 / 4.1 at 6000, 4.5 / 5.4 at 8192, 6.8 / 8.1 at
+    // 16384 (256 experts, 4096 tokens: 4.5 / 3.8).
+    if (n_experts <= 128 && n_tokens > kRsHalfTokens) {
+        if (n_experts <= 32) launch_bwd<2, 16>(a, s);
+        else if (n_experts <= 64) launch_bwd<4, 16>(a, s);
+        else launch_bwd<8, 16>(a, s);
+    } else if (n_experts <= 32) launch_bwd<1, 32>(a, s);
+    else if (n_experts <= 64) launch_bwd<2, 32>(a, s);
+    else if (n_experts <= 128) launch_bwd<4, 32>(a, s);
+    else if (n_experts <= 256) launch_bwd<8, 32>(a, s);
+    else if (n_experts <= 512) launch_bwd<16, 32>(a, s);
+    else launch_bwd<32, 32>(a, s);
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -221,6 +221,33 @@ def test_backward_repeated_unused_and_masked_slots():
             assert (d[3] == 0).all()
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("T,E,k,dtype,pad", [(4737, 128, 4, "bf16", 16), (4741, 33, 33, "f32", 0),
+                                             (5003, 100, 17, "f16", 1), (4801, 1, 1, "f32", 0), (4999, 31, 9, "bf16", 3)])
+def test_backward_of_many_tokens(score, normalize, T, E, k, dtype, pad):
+    """Up to 128 experts and above 4736 tokens half a warp has a token."""
+    l = _logits(T, E, dtype, T + E, pad=pad)
+    l[1, 1:] = -float("inf")
+    l[T - 1] = -float("inf")
+    g = torch.Generator().manual_seed(T)
+    ids = torch.rand(T, E, generator=g).topk(k, dim=1).indices.to(torch.int32)
+    ids[::3, 0] = ids[::3, k - 1]  # twice in a row
+    ids[::5, k // 2] = -1
+    ids[1::5, k // 2] = E
+    ids, dw = ids.cuda(), torch.randn(T, k, generator=g).cuda()
+    d = moe.route_scored_backward(l, ids, dw, score=score, normalize=normalize, scale=2.5)
+    half = torch.finfo(DT[dtype]).eps / 2
+    r, tol = ref.route_grad(l.double().cpu().numpy(), ids.cpu().numpy(), dw.double().cpu().numpy(), score, normalize,
+                            2.5, half)
+    err = np.abs(d.double().cpu().numpy() - r)
+    assert (err <= tol).all(), float((err / tol).max())
+    # the same rows by themselves, a warp each, are the same up to their roundings
+    few = moe.route_scored_backward(l[:70], ids[:70].contiguous(), dw[:70].contiguous(), score=score,
+                                    normalize=normalize, scale=2.5)
+    assert (np.abs(few.double().cpu().numpy() - r[:70]) <= tol[:70]).all()
+
+
 def test_rows_behind_the_last_token_are_left_alone():
     l = _logits(5, 64, "f32", 2)
     ids = torch.full((8, 4), -7, dtype=torch.int32).cuda()
