@@ -27,10 +27,14 @@
 // scales from shared to tensor memory, two issue the copies, one thread the
 // MMAs, one warp finds the units, four scatter the accumulators to dst.
 //
-// What bounds it: of the gate product 2.1 GB of weights and 0.27 GB of results
-// (6.2 TB/s at the boost clock, where the copy rate is 6.46; less when the power
-// limit lowers the SM clock); of shapes that reuse the weights from L2 the
-// latency of the stages, 7 in flight, against ~400 cycles of MMAs each.
+// What bounds it: the gate product (256 experts, 4096 tokens top-8, 7168 -> 2048:
+// 2.0 GB of weights, 0.27 of results, 0.12 of rounded rows) takes 381 us, 6.3 TB/s
+// where a copy reaches 6.46, and 440 where the power limit holds the SM clock at
+// 1.3 GHz.  A product whose experts' weights are read again from L2 (128 experts,
+// 8192 tokens top-4, 2880 -> 2880: 223 us) is bound by the way of a stage through
+// copies, scales and MMAs, 7 in flight: ~750 cycles a stage, of which ~260 are
+// MMAs; DRAM is at half its rate.  Weights asked into L2 ahead (by bulk prefetches
+// or by a warp's) made both slower: 274 and 426 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -503,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     }
 }
 
-// -------------------------------------------------------- quantising gather
+// ------------------------------------------------------------ rounding rows
 // Where the rounded rows go: codes [plane of 256 values][row][128 bytes], the
 // 16-byte chunk of block c at c ^ (row % 8); scales [plane][row], two words of
 // four scale bytes.
@@ -638,10 +642,11 @@ mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restric
             round_planes<TYPE>(x, r, n_in, kp, planes, slot_prow + r * copies, copies, o, lane);
 }
 
-// ------------------------------------------- row ids and gather in two launches
+// ------------------------------------------- tables and rounded rows in one launch
 // For up to kRidMaxE experts one launch of up to 148 CTAs makes the tables and
-// gathers, instead of the row-id pass and a gather (35 + 60 us of a 4096-token
-// gate product, 32 + 98 us of the skewed 8192-token one).  Each CTA counts the
+// rounds the rows, 54 us of the gate product above and 58 of the skewed one (the
+// row-id pass and a launch for the rows: 35 + 60 and 32 + 98).  The bytes bound it:
+// 58 MB read and 125 written, 189 and 50.  Each CTA counts the
 // slots by expert before its own and in all (the place of its first slot of
 // every expert, the tables' prefixes), ranks its slots in slot order - the same
 // stable counting sort - and rounds its rows straight into their tile rows.

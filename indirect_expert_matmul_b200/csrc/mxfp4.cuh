@@ -59,50 +59,4 @@ __device__ __forceinline__ void mx_values8(uint32_t w, float s, float (&v)[8]) {
     }
 }
 
-// Largest magnitude bit pattern of eight values, then of the four lanes (4i ..
-// 4i+3) that hold one block of 32; `mask` names the lanes taking part.
-__device__ __forceinline__ uint32_t mx_block_bits(const float (&v)[8], unsigned mask) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(mask, m, 1));
-    return max(m, __shfl_xor_sync(mask, m, 2));
-}
-
-// Eight consecutive elements at p (16-byte aligned when VEC) as float.
-template <bool VEC>
-__device__ __forceinline__ void mx_load8(const void* p, int type, float (&e)[8]) {
-    if (type == MOE_F32) {
-        const float* f = (const float*)p;
-        if (VEC) {
-            const float4 a = __ldg((const float4*)f), b = __ldg((const float4*)f + 1);
-            e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w;
-            e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = __ldg(f + i);
-        }
-        return;
-    }
-    uint32_t w[4];
-    if (VEC) {
-        const uint4 v = __ldg((const uint4*)p);
-        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-        const uint16_t* h = (const uint16_t*)p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(h + 2 * i) | (uint32_t)__ldg(h + 2 * i + 1) << 16;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (type == MOE_BF16) {
-            e[2 * i] = __uint_as_float(w[i] << 16);
-            e[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        } else {
-            e[2 * i] = __half2float(__ushort_as_half((unsigned short)(w[i] & 0xffffu)));
-            e[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(w[i] >> 16)));
-        }
-    }
-}
-
 }  // namespace moe
