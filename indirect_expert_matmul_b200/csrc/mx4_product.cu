@@ -852,20 +852,22 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
 }
 
 // ------------------------------------------------- few slots: one launch
-// Up to kMdMaxSlots slots the call is bound by launches and latency, and then
+// For up to kMdMaxSlots slots the call is bound by launches and latency, and then
 // by the touched experts' bytes, so one launch does it all: every CTA finds the
 // experts and their slots from the ids itself (up to kMdN slots of an expert
 // are a group), takes a contiguous range of (group, 128-row tile) items, rounds
 // its group's rows into shared memory - all of K, they are few - while the
 // weights already stream into a ring, and runs the MMAs 16 columns wide.
 // Roles: warp 0 copies weights, warp 1 issues the MMAs, warps 4-7 move the
-// weights' scales as the stages land, so that by the time warps 2, 3 and 8-11
+// weights' scales as the stages land, so that by the time warps 2, 3 and 8-19
 // have rounded the rows the ring is ready for the MMAs; warps 8-11 drain the
-// accumulator.
-constexpr int kMdThreads = 384;
-constexpr int kMdRounders = 6;      // warps 2, 3, 8-11
-constexpr int kMdMaxSlots = 128;
+// accumulator.  (With six rounding warps instead of fourteen: 31.5 us for 26.1, 64
+// slots on 8 experts, 4096 -> 4096; the same where a group has few rows.)
+constexpr int kMdThreads = 640;
+constexpr int kMdRounders = kMdThreads / 32 - 6;  // warps 2, 3 and from 8 on
+constexpr int kMdMaxSlots = 256;
 constexpr int kMdN = 16;            // columns of an accumulator
+static_assert(kMdMaxSlots <= kMdThreads, "a thread a slot");
 constexpr int kMdMaxPlanes = 36;    // K up to 9216
 constexpr int kMdKt = 8;            // k-steps of a stage: half the copies to issue, ~450 cycles a stage
 constexpr int kMdMaxStages = 5;
@@ -1140,7 +1142,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
         // Every warp here passes the same barriers: one that has given up says so at
         // the next, and all leave there.
         const int w = warp < 4 ? warp - 2 : warp - 6;
-        const bool drains = warp >= 8;
+        const bool drains = warp >= 8 && warp < 12;
         const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         constexpr int esz = TYPE == MOE_F32 ? 4 : 2;
         int group = -1;
@@ -1391,12 +1393,19 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     p.W = (const uint8_t*)W_prepared;
     p.L = WLayout(n_out, n_in, MOE_MXFP4);
     const int planes = (n_in + 255) / 256;
-    // One launch for few slots, unless they crowd on few experts (a group holds kMdN
-    // slots and streams its expert's weights again).  256 experts, top-8, 2048 -> 512,
-    // one launch / two: 14 / 21 us at 32 slots, 25 / 30 at 128, 35 / 38 at 256;
-    // 7168 -> 2048: 96 / 103 at 64, 217 / 213 at 256; 8 experts, top-8, 4096 -> 4096:
-    // 67 / 32 at 256.
-    const bool few = S <= kMdMaxSlots && S <= (int64_t)kMdN * n_experts && planes <= kMdMaxPlanes;
+    // One launch for few slots, unless they crowd on few experts: a group holds kMdN
+    // slots and streams its expert's weights again, and every CTA rounds its groups'
+    // rows itself (so by slots an expert times planes; the slots' square takes in that
+    // with more of them the other form's launches matter less).  us, one launch / two:
+    // 256 experts, 2048 -> 512: 9.5 / 17.6 at 32 slots, 20.7 / 25.8 at 128, 30.2 / 32.6
+    // at 256; 7168 -> 2048: 91.7 / 96.8 at 64, 162 / 162 at 160; 32 experts, 2048 ->
+    // 1024: 20.3 / 20.5 at 192, 22.6 / 20.7 at 256; 8 experts, 4096 -> 4096: 26.2 / 28.2
+    // at 64, 32.6 / 28.4 at 96; 8192 -> 4096: 40.7 / 41.8 at 40, 43.2 / 42.0 at 48;
+    // 1024 -> 1024: 10.5 / 14.4 at 128; one, 4096 -> 4096: 12.9 / 16.3 at 8, 17.4 / 16.6
+    // at 16.
+    const int64_t E = n_experts;
+    const bool few = S <= kMdMaxSlots && S <= kMdN * E && S * planes <= 160 * E && S * S * planes <= 10240 * E &&
+                     planes <= kMdMaxPlanes;
     if (!plan_weights(p, n_experts, few ? kMdKt : kMxStageKt)) return MOE_ERR_CUDA;
     p.out = dst;
     p.out_ld = n_out;

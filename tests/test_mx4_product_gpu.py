@@ -111,6 +111,24 @@ def test_slot_counts_at_the_borders_of_the_forms(S):
     _check(blocks, x, few, "per_slot")
 
 
+@pytest.mark.parametrize("S,n_in", [(129, 96), (200, 544), (255, 96), (256, 800), (257, 96)])
+def test_slot_counts_over_many_experts(S, n_in):
+    # up to 256 slots in one launch where the experts are many, however few of them are taken
+    E, n_out = 60, 200
+    blocks = _weights(E, n_out, n_in, S)
+    g = torch.Generator().manual_seed(S)
+    x = torch.randn(S, n_in, generator=g).to(torch.float16).cuda()
+    ids = torch.randint(0, E, (S, 1), generator=g, dtype=torch.int32)
+    _check(blocks, x, ids, "broadcast")
+    ids[: S - 3] = torch.randint(57, 59, (S - 3, 1), generator=g, dtype=torch.int32)
+    _check(blocks, x, ids, "per_slot")
+    ids[5] = E
+    ws = moe.workspace(S, 1, E, n_in, x_dtype=torch.float16)
+    W = moe.weights_prepare(blocks.cuda(), E, n_out, n_in, wtype="mxfp4")
+    moe.mul_mat_id_mx4(W, E, n_out, n_in, x, ids.cuda(), ws=ws)
+    assert moe.get_status(ws) == moe.ERR_BAD_ID
+
+
 @pytest.mark.parametrize("T", [3, 150])
 @pytest.mark.parametrize("stage", [0, 2])
 def test_expired_wait_reports_timeout_and_the_device_recovers(T, stage):
