@@ -209,8 +209,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     ptx::cluster_sync();  // both CTAs' barriers are set up
     ptx::tc_fence_after();
     const uint32_t tmem = uniform(s_tmem);
-    // (a programmatic dependent of the rounding: nothing it wrote is read before it has ended)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // (by one thread's reading: another CTA may set the status meanwhile; CTA 1 goes by CTA 0's units)
     if (tid == 0) s_total = read_status(status) != 0 ? 0 : p.hdr[kHdrTiles] * MU;
     if (in_smem)
@@ -505,6 +503,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         ptx::tc_fence_after();
         ptx::tmem_dealloc_pair(tmem, 512);
     }
+    // Tensor memory is given back by both CTAs together: neither leaves before the
+    // other has done its part, or the next CTA on its SM (another stream's) could ask
+    // for the memory in between.
+    __syncwarp();
+    ptx::cluster_sync();
 }
 
 // ------------------------------------------------------------ rounding rows
@@ -652,7 +655,7 @@ mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restric
 // stable counting sort - and rounds its rows straight into their tile rows.
 // Up to kMpSelfSlots slots every CTA reads all the ids.  Beyond, a launch before
 // counts the chunk of kMpParts CTAs and a CTA sums the chunks' counts and counts
-// its chunk's slots before its own, while that launch runs.  (The whole call
+// its chunk's slots before its own.  (The whole call
 // for 512 slots, 256 experts, 2048 -> 512: 42 us by itself, 46 with the launch
 // before; at 32768 slots there is no difference.)
 constexpr int kMpThreads = 1024;
@@ -684,7 +687,6 @@ __device__ __forceinline__ bool count_slots(const int32_t* __restrict__ ids, int
 __global__ void __launch_bounds__(kMpThreads)
 mx4_count_kernel(const int32_t* __restrict__ ids, int64_t T, int k, int E, int G, int32_t* __restrict__ counts, int* hdr) {
     extern __shared__ int s_cnt[];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (__syncthreads_or(threadIdx.x == 0 && read_status(hdr + kHdrStatus) != 0)) return;
     for (int e = threadIdx.x; e < E; e += kMpThreads) s_cnt[e] = 0;
     __syncthreads();
@@ -741,21 +743,17 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
     for (int e = tid; e < E; e += kMpThreads) s_base[e] = s_row[e] = 0;
     __syncthreads();
     if (!p.counts) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
         const bool stop = tid == 0 && read_status(p.hdr + kHdrStatus) != 0;
         bool bad = count_slots(p.ids, 0, (int)(t0 * k), E, s_base);
         bad |= count_slots(p.ids, (int)(t0 * k), (int)(p.T * k), E, s_row);
         if (bad) set_status(p.hdr + kHdrStatus, MOE_ERR_BAD_ID);
         if (__syncthreads_or(bad || stop)) return;
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (tid < E) all = s_base[tid] + s_row[tid];
+            if (tid < E) all = s_base[tid] + s_row[tid];
         __syncthreads();
     } else {
         const int chunk = g / kMpParts, C = (G + kMpParts - 1) / kMpParts;
         count_slots(p.ids, (int)(mp_token(p.T, chunk * kMpParts, G) * k), (int)(t0 * k), E, s_base);
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (__syncthreads_or(tid == 0 && read_status(p.hdr + kHdrStatus) != 0)) return;
+            if (__syncthreads_or(tid == 0 && read_status(p.hdr + kHdrStatus) != 0)) return;
         // 1024 / E threads an expert, each some of the chunks
         const int Ep = (E + 31) & ~31, parts = kMpThreads / Ep;
         const int e = tid % Ep, part = tid / Ep;
@@ -948,9 +946,6 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
         ptx::tmem_alloc(&s_tmem, 512);
         ptx::tmem_relinquish();
     }
-    // (starts before the stream's previous kernel has ended, and lets the next one do so)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 3 && lane < 4) {
         // this CTA's share of x into L2, while the groups are found
         const int64_t all = (int64_t)(a.per_slot ? S : S / a.k) * a.n_in * (TYPE == MOE_F32 ? 4 : 2);
@@ -1311,21 +1306,14 @@ bool plan_weights(Mx4Params& p, int n_experts, int stage_kt) {
     return true;
 }
 
-// A launch that may start before the stream's previous kernel has ended (which
-// lets it, by griddepcontrol.launch_dependents) and waits for it itself.
+// An ordinary launch: no kernel here starts before its stream's previous one has
+// ended.  (Launched as programmatic dependents, the next kernel's blocks set up
+// meanwhile, calls on three streams at once came to a standstill after some hundred
+// thousand; no block holds an SM, or its tensor memory, waiting for another grid.)
 template <typename A>
-moe_status launch_dependent(void (*kernel)(A), unsigned grid, int threads, size_t smem, cudaStream_t stream, const A& args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+moe_status launch(void (*kernel)(A), unsigned grid, int threads, size_t smem, cudaStream_t stream, const A& args) {
+    kernel<<<grid, threads, smem, stream>>>(args);
+    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // The kernel's shared-memory limit, set once a device.
@@ -1344,7 +1332,7 @@ template <int TYPE>
 moe_status launch_place(const MxPlaceArgs& a, unsigned grid, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     if (!allow_smem(mx4_place_kernel<TYPE>, (int)(34 * kRidMaxE * sizeof(int)), done)) return MOE_ERR_CUDA;
-    return launch_dependent(mx4_place_kernel<TYPE>, grid, kMpThreads, smem, s, a);
+    return launch(mx4_place_kernel<TYPE>, grid, kMpThreads, smem, s, a);
 }
 
 template <int TYPE>
@@ -1353,7 +1341,7 @@ moe_status launch_decode(const MxDecodeArgs& a, cudaStream_t s) {
     if (!allow_smem(mx4_decode_kernel<TYPE>, (int)kMdSmem, done)) return MOE_ERR_CUDA;
     const int64_t items = (int64_t)a.S * a.w.L.mt_count;  // at most: a group has a slot
     const int sms = mx_sm_count();
-    return launch_dependent(mx4_decode_kernel<TYPE>, (unsigned)(items < sms ? items : sms), kMdThreads, kMdSmem, s, a);
+    return launch(mx4_decode_kernel<TYPE>, (unsigned)(items < sms ? items : sms), kMdThreads, kMdSmem, s, a);
 }
 
 moe_status launch_mx4_gemm(const Mx4Params& p, int64_t max_coltiles, cudaStream_t stream) {
@@ -1362,7 +1350,7 @@ moe_status launch_mx4_gemm(const Mx4Params& p, int64_t max_coltiles, cudaStream_
     const int64_t units = max_coltiles * ((p.L.mt_count + 1) / 2);
     const int pairs = mx_sm_count() / 2;
     const unsigned grid = 2u * (unsigned)(units < pairs ? units : pairs);
-    return launch_dependent(mx4_gemm_kernel, grid, kMxThreads, kMxSmem, stream, p);
+    return launch(mx4_gemm_kernel, grid, kMxThreads, kMxSmem, stream, p);
 }
 
 }  // namespace

@@ -193,6 +193,37 @@ def test_two_calls_at_once_on_two_streams():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+def test_many_calls_at_once_on_three_streams():
+    # both forms, the general tables and the counted ones, with one another and with other kernels
+    jobs = []
+    for T, E, k, n_in, n_out in ((4, 64, 8, 512, 256), (300, 32, 4, 256, 300), (90, 1100, 4, 256, 64),
+                                 (9000, 8, 4, 64, 128)):
+        W = moe.weights_prepare(_weights(E, n_out, n_in, T).cuda(), E, n_out, n_in, wtype="mxfp4")
+        g = torch.Generator().manual_seed(T)
+        x = torch.randn(T, n_in, generator=g).bfloat16().cuda()
+        ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32).cuda()
+        args = (W, E, n_out, n_in, x, ids)
+        jobs.append((args, moe.mul_mat_id_mx4(*args)))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    ws = [[moe.workspace(a[5].shape[0], a[5].shape[1], a[1], a[3]) for a, _ in jobs] for _ in streams]
+    outs = [[torch.empty_like(want) for _, want in jobs] for _ in streams]
+    differ = [torch.zeros(1, dtype=torch.int64).cuda() for _ in streams]
+    order = torch.randint(0, 12, (12000,), generator=torch.Generator().manual_seed(1)).tolist()
+    torch.cuda.synchronize()
+    for n, c in enumerate(order):
+        i, j = c % 3, c // 3
+        args, want = jobs[j]
+        with torch.cuda.stream(streams[i]):
+            moe.mul_mat_id_mx4(*args, ws=ws[i][j], out=outs[i][j])
+            if n % 7 == 0:
+                differ[i] += (outs[i][j] != want).any()
+        if n % 60 == 59:
+            torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    assert [int(d.item()) for d in differ] == [0, 0, 0]
+    assert all(moe.get_status(w) == moe.OK for row in ws for w in row)
+
+
 def test_one_expert_takes_all_and_most_take_none():
     blocks = _weights(64, 64, 192, 1)
     x = torch.randn(600, 192, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
