@@ -657,7 +657,7 @@ mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restric
 // counts the chunk of kMpParts CTAs and a CTA sums the chunks' counts and counts
 // its chunk's slots before its own.  (The whole call
 // for 512 slots, 256 experts, 2048 -> 512: 42 us by itself, 46 with the launch
-// before; at 32768 slots there is no difference.)
+// before, which pays where a CTA would count many more.)
 constexpr int kMpThreads = 1024;
 constexpr int kMpMaxCtas = 148, kMpParts = 4;
 constexpr int64_t kMpSelfSlots = 32768;
@@ -1385,14 +1385,14 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
     // slots and streams its expert's weights again, and every CTA rounds its groups'
     // rows itself (so by slots an expert times planes; the slots' square takes in that
     // with more of them the other form's launches matter less).  us, one launch / two:
-    // 256 experts, 2048 -> 512: 9.5 / 17.6 at 32 slots, 20.7 / 25.8 at 128, 30.2 / 32.6
-    // at 256; 7168 -> 2048: 91.7 / 96.8 at 64, 162 / 162 at 160; 32 experts, 2048 ->
-    // 1024: 20.3 / 20.5 at 192, 22.6 / 20.7 at 256; 8 experts, 4096 -> 4096: 26.2 / 28.2
-    // at 64, 32.6 / 28.4 at 96; 8192 -> 4096: 40.7 / 41.8 at 40, 43.2 / 42.0 at 48;
-    // 1024 -> 1024: 10.5 / 14.4 at 128; one, 4096 -> 4096: 12.9 / 16.3 at 8, 17.4 / 16.6
+    // 256 experts, 2048 -> 512: 9.2 / 18.7 at 32 slots, 20.9 / 27.7 at 128, 30.5 / 34.7
+    // at 256; 7168 -> 2048: 91.3 / 99.0 at 64, 163 / 163 at 160; 32 experts, 2048 ->
+    // 1024: 20.3 / 22.3 at 192, 22.2 / 22.2 at 256; 8 experts, 4096 -> 4096: 26.7 / 30.3
+    // at 80 slots, 31.9 / 30.1 at 96; 8192 -> 4096: 40.3 / 43.9 at 40, 42.8 / 44.2 at 48;
+    // 1024 -> 1024: 10.5 / 15.8 at 128; one, 4096 -> 4096: 12.9 / 18.1 at 8, 17.2 / 18.3
     // at 16.
     const int64_t E = n_experts;
-    const bool few = S <= kMdMaxSlots && S <= kMdN * E && S * planes <= 160 * E && S * S * planes <= 10240 * E &&
+    const bool few = S <= kMdMaxSlots && S <= kMdN * E && S * planes <= 200 * E && S * S * planes <= 12800 * E &&
                      planes <= kMdMaxPlanes;
     if (!plan_weights(p, n_experts, few ? kMdKt : kMxStageKt)) return MOE_ERR_CUDA;
     p.out = dst;
