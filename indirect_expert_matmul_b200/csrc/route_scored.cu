@@ -352,7 +352,9 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const Route
                 float a, c;
                 group_top2<NPL>(group_key, lane, E, size, g, a, c);
                 if (lane == g) mine = p.group_top == 2 ? __fadd_rn(a, c) : a;
-                if (BIAS && p.group_top == 2) mag = fmaxf(mag, fabsf(a) + fabsf(c));
+                // (a group without two finite keys takes no part: its sum is -inf whatever its roundings)
+                const float terms = fabsf(a) + fabsf(c);
+                if (BIAS && p.group_top == 2 && terms < INFINITY) mag = fmaxf(mag, terms);
             }
         }
         int rank = 0;  // groups ahead of this lane's
