@@ -323,11 +323,15 @@ MOE_API moe_status moe_route(const float *logits, const float *bias, int64_t n_t
  *   weights[t][i] = scale * s[ids[i]], divided by the sum of the k chosen s when
  *                   normalize != 0                        (float [n_tokens][k])
  * n_groups = topk_groups = 1 chooses among all experts.  The choice follows the
- * rule over real numbers (keys that close float values cannot tell apart are
- * compared in double); without a bias equal logits are equal keys.  Weights are
+ * rule over real numbers as far as double precision tells keys apart: keys that
+ * close float values cannot order are worked out again in double, each score as
+ * its distance from 0, 1/2 or 1 (softmax: from 0 or the largest score), so that
+ * scores which round to one value, a sigmoid's above 37 to 1, keep the order of
+ * their logits; keys equal then go to the lower expert.  Without a bias equal
+ * logits are equal keys.  bias: finite, or -inf, behind every finite key.  Weights are
  * evaluated in float relative to the largest logit involved, so normalised
  * weights stay finite and sum to scale however far the logits are from zero:
- * within (span + 16 + n_experts + k) * 2^-24 relative of the exact value, span
+ * within (span + 16 + n_experts + k) * 2^-24 relative (and 2^-149) of the exact value, span
  * the largest minus the smallest finite logit involved.  A logit of -inf has
  * score 0 (and key bias[e]); where all scores of a sum are 0 the weights are 0.
  * NaN or +inf logits: ids are still k distinct experts of open groups, weights

@@ -13,7 +13,7 @@
 // The choice is that of the rule over real numbers.  Float keys carry a bound on
 // their error; wherever two of them are closer than that, the candidates (or
 // the groups) are compared again in double, so that the choice does not depend
-// on how a float was rounded.  Without a bias the order of the scores is that
+// on how a float was rounded, nor on a score that rounds to 0, 1/2 or 1.  Without a bias the order of the scores is that
 // of the logits, which are compared as they are.
 //
 // One warp per token, NPL consecutive experts a lane (E <= 32 NPL), read once
@@ -159,14 +159,32 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[NPL], int (&idx)[NPL])
                 }
 }
 
+// A key in two doubles, hi + lo exactly what their sum says and hi the sum rounded.
+struct Key {
+    double hi, lo;
+    // hi and lo of a + b (exact) + c
+    static __device__ Key sum(double a, double b, double c) {
+        const double h = __dadd_rn(a, b), bb = __dsub_rn(h, a);
+        const double r = __dadd_rn(__dadd_rn(__dsub_rn(a, __dsub_rn(h, bb)), __dsub_rn(b, bb)), c);
+        const double hi = __dadd_rn(h, r), rr = __dsub_rn(hi, h);
+        const double lo = __dadd_rn(__dsub_rn(h, __dsub_rn(hi, rr)), __dsub_rn(r, rr));
+        if (fabs(hi) < INFINITY) return {hi, lo};
+        return {h == h ? h : -INFINITY, 0.0};  // an infinite bias; NaN counts as the lowest
+    }
+    __device__ bool operator>(const Key& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
+    __device__ bool operator==(const Key& o) const { return hi == o.hi && lo == o.lo; }
+};
+
 // The double-precision side of a token, for close keys only, one expert at a
 // time: kept in registers and unrolled over the lane's experts it took so many
-// that the 4096-token prompt of 256 experts ran in 29 us.
+// that the 4096-token prompt of 256 experts ran in 29 us.  A score is worked out
+// as its distance from 0, 1/2 or 1 (softmax: from 0 or the largest score), so
+// that scores which round to one double, a sigmoid's above 37 to 1, keep their order.
 struct Exact {
     const RouteScoredArgs& p;
     int64_t row;
     float mx;     // softmax: the largest logit
-    double* key;  // [n_experts]
+    double* key;  // [n_experts]: the keys' hi
     double z;     // softmax: the denominator
 
     __device__ void denominator(int lane) {
@@ -179,25 +197,49 @@ struct Exact {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     }
-    __device__ double key_of(int e) const {
+    __device__ Key key_of(int e) const {
         const float l = load_logit(p.logits, p.type, row + e);
-        double s = 0.0;
+        const double b = p.bias ? (double)__ldg(p.bias + e) : 0.0;
+        double base = 0.0, rest = 0.0;
         if (l != -INFINITY) {
-            const double x = exp(p.softmax ? (double)l - (double)mx : -(double)l);
-            s = p.softmax ? x / z : 1.0 / (1.0 + x);
+            // r = exp of -|l| or of l - mx, m = r - 1 without its cancellation
+            const double x = p.softmax ? (double)l - (double)mx : -fabs((double)l), r = exp(x);
+            const double m = x > -0x1p-10 ? x * (1.0 + x * (0.5 + x * (1.0 / 6 + x * (1.0 / 24)))) : r - 1.0;
+            const double big = 1.0 / (p.softmax ? z : 1.0 + r);
+            if (p.softmax) {
+                base = x > -0.5 ? big : 0.0;
+                rest = big * (x > -0.5 ? m : r);
+            } else if (x > -1.0) {  // 1 / (1 + exp(-l)) - 1/2 = (1 - exp(-|l|)) / (1 + exp(-|l|)) / 2, signed
+                base = 0.5;
+                rest = copysign(0.5 * m * big, (double)l);
+            } else {
+                base = l > 0.f ? 1.0 : 0.0;
+                rest = r * big;
+                if (l > 0.f) rest = -rest;
+            }
         }
-        if (p.bias) s += (double)__ldg(p.bias + e);
-        return s == s ? s : -INFINITY;
+        return Key::sum(base, b, rest);
     }
     __device__ void fill(int lane) {
         denominator(lane);
 #pragma unroll 1
-        for (int e = lane; e < p.n_experts; e += 32) key[e] = key_of(e);
+        for (int e = lane; e < p.n_experts; e += 32) key[e] = key_of(e).hi;
         __syncwarp();
     }
-    // Lane g: the score of group g.
-    __device__ double group_score(int lane, int size) const {
+    // Whether expert e with the high part v comes before f with w (kNone: no
+    // expert): the larger key, equal keys by the lower index.
+    static constexpr int kNone = 0x7fffffff;
+    __device__ bool before(double v, int e, double w, int f) const {
+        if (v != w || e == kNone || f == kNone) return e != kNone && (f == kNone || v > w);
+        const float l = load_logit(p.logits, p.type, row + e), o = load_logit(p.logits, p.type, row + f);
+        if (l == o && (!p.bias || __ldg(p.bias + e) == __ldg(p.bias + f))) return e < f;
+        const double a = key_of(e).lo, b = key_of(f).lo;
+        return a > b || (a == b && e < f);
+    }
+    // Lane g: the score of group g as one double; mag: the largest magnitude of terms.
+    __device__ double group_score(int lane, int size, double& mag) const {
         double mine = -INFINITY;
+        mag = 0.0;
 #pragma unroll 1
         for (int g = 0; g < p.n_groups; ++g) {
             double a = -INFINITY, b = -INFINITY;
@@ -213,7 +255,43 @@ struct Exact {
                 b = fmax(fmax(b, ob), fmin(a, oa));
                 a = fmax(a, oa);
             }
+            const double terms = p.group_top == 2 ? fabs(a) + fabs(b) : fabs(a);
+            if (terms < INFINITY) mag = fmax(mag, terms);
             if (lane == g) mine = p.group_top == 2 ? a + b : a;
+        }
+        return mine;
+    }
+    // The same with the rests (~2 us a token, for groups that the doubles leave close).
+    __device__ Key group_key(int lane, int size) const {
+        Key mine = {-INFINITY, 0.0};
+#pragma unroll 1
+        for (int g = 0; g < p.n_groups; ++g) {
+            double a = -INFINITY, b = -INFINITY;  // the group's two first, ea and eb
+            int ea = kNone, eb = kNone;
+            auto take = [&](double v, int e) {
+                if (before(v, e, a, ea)) {
+                    b = a; eb = ea;
+                    a = v; ea = e;
+                } else if (before(v, e, b, eb)) {
+                    b = v; eb = e;
+                }
+            };
+#pragma unroll 1
+            for (int e = g * size + lane; e < (g + 1) * size; e += 32) take(key[e], e);
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1) {
+                const double oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+                const int oea = __shfl_xor_sync(0xffffffffu, ea, o), oeb = __shfl_xor_sync(0xffffffffu, eb, o);
+                take(oa, oea);
+                take(ob, oeb);
+            }
+            if (lane == g) {
+                mine = key_of(ea);
+                if (p.group_top == 2) {
+                    const Key second = key_of(eb);
+                    mine = Key::sum(mine.hi, second.hi, __dadd_rn(mine.lo, second.lo));
+                }
+            }
         }
         return mine;
     }
@@ -223,21 +301,21 @@ struct Exact {
 #pragma unroll 1
         for (int i = 0; i < p.k; ++i) {
             double best = -INFINITY;
-            int be = 0x7fffffff, q = 0;
+            int be = kNone, q = 0;
 #pragma unroll 1
             for (int e = lane; e < p.n_experts; e += 32, ++q) {
                 const double v = key[e];
                 if ((taken >> q & 1u) || !(open >> (e / size) & 1u)) continue;
-                if (be == 0x7fffffff || v > best) {
+                if (before(v, e, best, be)) {
                     best = v;
                     be = e;
                 }
             }
-#pragma unroll
+#pragma unroll 1
             for (int o = 16; o > 0; o >>= 1) {
                 const double ov = __shfl_xor_sync(0xffffffffu, best, o);
                 const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-                if (oe != 0x7fffffff && (be == 0x7fffffff || ov > best || (ov == best && oe < be))) {
+                if (before(ov, oe, best, be)) {
                     best = ov;
                     be = oe;
                 }
@@ -272,8 +350,10 @@ __device__ __forceinline__ void group_top2(const F& value, int lane, int E, int 
     }
 }
 
+// (registers: the double-precision side would take up to 72 everywhere; held to
+// what the float side needs, it spills: 8191 x 128 softmax without a bias 7.1 us for 7.4)
 template <int NPL, bool BIAS>
-__global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const RouteScoredArgs p) {
+__global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 10 : NPL == 8 ? 8 : 1) route_scored_kernel(const RouteScoredArgs p) {
     __shared__ double s_key[kRsWarps][32 * NPL];
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRsWarps + (threadIdx.x >> 5);
@@ -373,11 +453,26 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const Route
             const float terms = 1.2e-7f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(own)));
             if (hi >= rival(lo, 2.f * err + terms) && lo > ordered(-INFINITY)) {
                 exact64.fill(lane);
-                const double best = exact64.group_score(lane, size);
+                double mag64;
+                const double best = exact64.group_score(lane, size, mag64);
                 rank = 0;
+                double next = -INFINITY;  // the best score that is not ahead of this lane's
                 for (int g = 0; g < G; ++g) {
                     const double o = __shfl_sync(0xffffffffu, best, g);
-                    rank += o > best || (o == best && g < lane);
+                    const bool ahead = o > best || (o == best && g < lane);
+                    rank += ahead;
+                    if (!ahead && g != lane) next = fmax(next, o);
+                }
+                // (roundings of the terms, 2^-53 each, and of their sum)
+                const bool near = lane < G && rank == p.topk_groups - 1 && next > -INFINITY &&
+                                  best - next <= 0x1p-50 * (1.0 + mag64);
+                if (__any_sync(0xffffffffu, near)) {
+                    const Key full = exact64.group_key(lane, size);
+                    rank = 0;
+                    for (int g = 0; g < G; ++g) {
+                        const Key o = {__shfl_sync(0xffffffffu, full.hi, g), __shfl_sync(0xffffffffu, full.lo, g)};
+                        rank += o > full || (o == full && g < lane);
+                    }
                 }
                 in = lane < G && rank < p.topk_groups;
             }
@@ -462,11 +557,11 @@ __global__ void __launch_bounds__(kRsWarps * 32) route_scored_kernel(const Route
             }
             if (n <= 32 && (rest == 0u || rest < rival(before, err))) {
                 exact64.denominator(lane);
-                const double v = lane < n ? exact64.key_of(my_id) : 0.0;
+                const Key v = lane < n ? exact64.key_of(my_id) : Key{0.0, 0.0};
                 int place = 0;
 #pragma unroll 1
                 for (int j = 0; j < n; ++j) {
-                    const double o = __shfl_sync(0xffffffffu, v, j);
+                    const Key o = {__shfl_sync(0xffffffffu, v.hi, j), __shfl_sync(0xffffffffu, v.lo, j)};
                     const int oe = __shfl_sync(0xffffffffu, my_id, j);
                     place += o > v || (o == v && oe < my_id);
                 }
