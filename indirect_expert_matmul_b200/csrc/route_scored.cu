@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 10 :
     if (BIAS) {  // and the last against the best of the rest
         uint32_t rest = __reduce_max_sync(0xffffffffu, key[0]);
         if (__any_sync(0xffffffffu, close || (rest != 0u && rest >= rival(before, err)))) {
+            __syncwarp();  // other lanes write the entries of it[] again
             // Draw on until a gap, so that the list holds every expert that may belong to
             // the k; order it by double keys, one lane an entry (~0.5 us for the token).
             int n = p.k;

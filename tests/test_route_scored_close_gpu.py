@@ -101,3 +101,15 @@ def test_all_keys_equal():
             ids, _ = moe.route_scored(l, 40, bias=torch.full((256,), bias).cuda(), n_groups=8, topk_groups=4,
                                       group_score="top2")
             assert (ids == torch.arange(40).cuda()).all()
+
+
+@pytest.mark.parametrize("E,k", [(96, 24), (160, 60)])
+def test_reordered_choices_of_many_tokens(E, k):
+    # every token's first order is put right by other lanes than those that wrote it
+    T = 4096
+    g = torch.Generator().manual_seed(k)
+    l = (torch.randn(T, E, generator=g) * 1e-6).cuda()
+    b = (0.25 + torch.randint(0, 2, (E,), generator=g).float() * 2.0 ** -23)
+    ids, _ = moe.route_scored(l, k, bias=b.cuda())
+    key = 0.5 * torch.tanh(0.5 * l.double()) + b.double().cuda()  # (1/2 less: exact to 1e-17)
+    assert torch.equal(ids.long(), torch.sort(key, dim=1, descending=True, stable=True).indices[:, :k])
