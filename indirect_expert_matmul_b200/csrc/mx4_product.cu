@@ -201,14 +201,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
         s_abort = 0;
         ptx::fence_mbar_init();
     }
+    // The pair allocates tensor memory together, once both CTAs run: an SM has room
+    // for one CTA of this library's tensor-memory users (145 KB of shared memory and
+    // more each), so what it waits for here is given back by a CTA that has ended.
+    ptx::cluster_sync();
     if (warp == 1) {
         ptx::tmem_alloc_pair(&s_tmem, 512);
         ptx::tmem_relinquish_pair();
     }
-    ptx::tc_fence_before();
-    ptx::cluster_sync();  // both CTAs' barriers are set up
-    ptx::tc_fence_after();
-    const uint32_t tmem = uniform(s_tmem);
     // (by one thread's reading: another CTA may set the status meanwhile; CTA 1 goes by CTA 0's units)
     if (tid == 0) s_total = read_status(status) != 0 ? 0 : p.hdr[kHdrTiles] * MU;
     if (in_smem)
@@ -217,7 +217,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
             s_bounds[i] = p.bounds[i];
             s_pad[i] = p.pad_start[i];
         }
-    __syncthreads();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();  // both CTAs' barriers, tensor memory and tables are set up
+    ptx::tc_fence_after();
+    const uint32_t tmem = uniform(s_tmem);
     const int total = uniform(s_total);
 
     // Unit t, by a whole warp: the largest group whose first column tile is at most
