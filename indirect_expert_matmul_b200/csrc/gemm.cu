@@ -595,6 +595,7 @@ grouped_gemm_kernel(const GemmParams p) {
                     const int c0 = (4 * q + wj) * 16;
                     if (c0 >= tl.n) break;
                     uint32_t v[16], u[16];
+                    __syncwarp();  // (tensor memory is read by the whole warp)
                     ptx::tmem_ld_32x32b_x16(tmem_base + lanes + c0, v);
                     ptx::tmem_ld_32x32b_x16(tmem_base + lanes + kAccCols + c0, u);
                     ptx::tmem_ld_wait();
@@ -621,6 +622,7 @@ grouped_gemm_kernel(const GemmParams p) {
                         const int c0 = (4 * q + wj) * 16;
                         if (c0 >= tl.n) break;
                         uint32_t v[16];
+                        __syncwarp();
                         ptx::tmem_ld_32x32b_x16(tmem_base + lanes + (uint32_t)i * kAccCols + c0, v);
                         ptx::tmem_ld_wait();
 #pragma unroll

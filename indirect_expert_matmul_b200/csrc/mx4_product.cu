@@ -467,12 +467,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
             // A column is a sorted row: its 32 lanes are 128 consecutive bytes of one
             // row of dst.  The rows' numbers come from shared memory, four to a load: by
             // shuffles under a test a column cost 105 cycles.
+            // (Tensor memory is read by the whole warp: the lanes meet again after their stores.)
             for (int c0 = 0; c0 < n; c0 += 32) {
                 uint32_t v[32];
+                __syncwarp();
                 ptx::tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * wq) << 16) + buf * kMxBN + c_lo + c0, v);
                 ptx::tmem_ld_wait();
-                if (!m_ok) continue;
-                if (c0 + 32 <= n) {
+                if (m_ok && c0 + 32 <= n) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const int4 r = *(const int4*)(rows + c0 + j);
@@ -481,14 +482,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                         out[(int64_t)r.z * p.out_ld] = __uint_as_float(v[j + 2]);
                         out[(int64_t)r.w * p.out_ld] = __uint_as_float(v[j + 3]);
                     }
-                } else {
+                } else if (m_ok) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (c0 + j < n) out[(int64_t)rows[c0 + j] * p.out_ld] = __uint_as_float(v[j]);
                 }
             }
-            ptx::tc_fence_before();
             __syncwarp();
+            ptx::tc_fence_before();
             if (lane == 0) ptx::mbar_arrive_cluster<false>(&acc_empty[buf], 0);
         }
     }
@@ -1219,8 +1220,8 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
                             p.out[(int64_t)(slots[j / 2] >> (16 * (j & 1)) & 0xffffu) * p.out_ld + m] =
                                 __uint_as_float(v[j]);
                 }
-                ptx::tc_fence_before();
                 __syncwarp();
+                ptx::tc_fence_before();
                 if (lane == 0) ptx::mbar_arrive(&acc_empty[buf]);
             }
         }

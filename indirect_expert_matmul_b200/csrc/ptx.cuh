@@ -103,8 +103,10 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t pari
 
 // Named-barrier reduction: the `count` threads (whole warps) meet at barrier
 // `id`; every one receives the AND of their `v`.  No shared-memory access.
+// (an aligned barrier: the warp's lanes meet first)
 __device__ __forceinline__ bool bar_red_and(uint32_t id, uint32_t count, bool v) {
     uint32_t r;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred pi, po;\n\t"
         "setp.ne.u32 pi, %1, 0;\n\t"
