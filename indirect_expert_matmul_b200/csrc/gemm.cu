@@ -233,7 +233,8 @@ grouped_gemm_kernel(const GemmParams p) {
     __shared__ int s_bounds[kSmemGroups + 1];
     __shared__ int s_pad[kSmemGroups + 1];
 
-    if (read_status(p.hdr + kHdrStatus) != 0) return;
+    // (one thread's reading for all: a CTA of this launch that gives up sets the word meanwhile)
+    if (__syncthreads_or(threadIdx.x == 0 && read_status(p.hdr + kHdrStatus) != 0)) return;
 
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_dyn + 1023) & ~(uintptr_t)1023);
     uint8_t* sB = smem + Cfg::b_off;
