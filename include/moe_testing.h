@@ -34,8 +34,12 @@ extern "C" {
  * every bounded wait of those launches gives up after `wait_us` microseconds.
  * The warp that waits for the MMA warp's operands then gives up, hands the
  * failure to the MMA warp through their named barrier, and the launch ends the
- * same way (status MOE_ERR_TIMEOUT, the site in header word 3).  Not
- * thread-safe; not for production use.
+ * same way (status MOE_ERR_TIMEOUT, the site in header word 3).  So it does to
+ * the 4-bit product (moe_mul_mat_id_mx4): the rows' copy of a stage of CTA `cta`,
+ * in the one-launch form the weights'.  A CTA number that no launch has only
+ * shortens the waits; a wait sleeps up to 20 us before it looks at its limit,
+ * and those for copies and MMAs in flight keep theirs.  Not thread-safe; not for
+ * production use.
  */
 MOE_API void moe_testing_stall(int cta, int stage, int wait_us);
 

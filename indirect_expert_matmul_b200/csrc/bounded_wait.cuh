@@ -8,7 +8,9 @@
 
 namespace moe {
 
-constexpr long long kWaitLimitCycles = 1ll << 32; // ~2 s
+// ~2 s.  The waits for a CTA's own copies and MMAs before it leaves keep this limit
+// where a test shortens the others: what is in flight lands.
+constexpr long long kWaitLimitCycles = 1ll << 32;
 constexpr uint32_t kSleepNs = 20000; // upper bound of one hardware wait
 
 __device__ __forceinline__ void expired(uint64_t* bar, volatile int* abort_flag, int* status) {

@@ -363,7 +363,7 @@ grouped_gemm_kernel(const GemmParams p) {
             // let every copy issued land before the CTA can exit (bounded)
             volatile int never = 0;
             for (int s = 0; s < kRS; ++s)
-                if (used >> s & 1) wait_bar(&raw_full[s], (par >> s) & 1, &never, status, p.wait_limit);
+                if (used >> s & 1) wait_bar(&raw_full[s], (par >> s) & 1, &never, status, kWaitLimitCycles);
         }
     } else if (warp == kWarpProdB) {
         // ------------------------------------------------ activation producer
@@ -394,7 +394,7 @@ grouped_gemm_kernel(const GemmParams p) {
             }
             volatile int never = 0;
             for (int s = 0; s < kMB; ++s)
-                if (used >> s & 1) wait_bar(&b_full[s], (par >> s) & 1, &never, status, p.wait_limit);
+                if (used >> s & 1) wait_bar(&b_full[s], (par >> s) & 1, &never, status, kWaitLimitCycles);
         }
     } else if (warp == kWarpMma) {
         // ----------------------------------------------------------------- MMA
@@ -440,7 +440,7 @@ grouped_gemm_kernel(const GemmParams p) {
         if (lane == 0) {
             ptx::mma_commit(mma_drained);
             volatile int never = 0;
-            wait_bar(mma_drained, 0, &never, status, p.wait_limit);
+            wait_bar(mma_drained, 0, &never, status, kWaitLimitCycles);
         }
         __syncwarp();
     } else if (warp == kWarpWait) {

@@ -545,7 +545,7 @@ __device__ __forceinline__ void gemv_body(const GemvArgs& a) {
             const uint32_t first = sc > (uint32_t)a.ns ? sc - a.ns : 0u;
             for (uint32_t q = first; q < sc; ++q)
                 if (!((int)blockIdx.x == a.stall_cta && (int)q == a.stall_stage))
-                    gv_wait(&full[q % a.ns], (q / a.ns) & 1u, status, &never, a.wait_limit);
+                    gv_wait(&full[q % a.ns], (q / a.ns) & 1u, status, &never, kGvWaitLimit);  // (a test shortens the others)
         }
         return;
     }

@@ -161,6 +161,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     __shared__ int s_next[2 * kMxUnits];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_total;
+    __shared__ int s_issued[2];  // stages whose weights, whose rows have been asked for
 
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_dyn + 1023) & ~(uintptr_t)1023);
     uint64_t* full = (uint64_t*)(smem + kMxBarOff);  // a stage's copies have landed
@@ -260,13 +261,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     if (warp == 0) {
         // ------------------------------------------------------------ weights
         const uint32_t issue = ptx::elect_one();
-        int s = 0;
-        uint32_t ph = 0, used = 0, par = 0;
+        int s = 0, q = 0;
+        uint32_t ph = 0;
         bool ok = true;
         MxTile u;
         for (int k = 0; ok && take_unit(k, u); ++k) {
             const int mt = u.mu * 2 + (int)rank;
-            for (int ks = 0; ks < KS; ++ks) {
+            for (int ks = 0; ks < KS; ++ks, ++q) {
                 ok = warp_wait(&empty[s], ph ^ 1, abort_flag, status, p.wait_limit);
                 if (!ok) break;
                 uint8_t* st = smem + s * kMxStagePitch;
@@ -274,16 +275,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                     if (mt < MT) load_weights<kMxStageKt>(p, L, st, st + kMxOffAS, u.e, mt, ks, &full[s]);
                     else ptx::mbar_arrive(&full[s]);
                 }
-                used |= 1u << s;
-                par = (par & ~(1u << s)) | (ph << s);
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
         }
-        // let every copy issued land before the CTA can exit (bounded): a stage
-        // completes when all warps' copies have
-        volatile int never = 0;
-        for (int j = 0; j < kMxStages; ++j)
-            if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, p.wait_limit);
+        if (lane == 0) s_issued[0] = q;
     } else if (warp == 2) {
         // --------------------------------------------------------------- rows
         // This CTA's half of the unit's rows (contiguous and swizzled) and every
@@ -312,6 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
                 if (++s == kMxStages) { s = 0; ph ^= 1; }
             }
         }
+        if (lane == 0) s_issued[1] = q;
     } else if (warp == 3) {
         // -------------------------------------------------------------- units
         // A pair's first unit goes by its number, every further one is the next that no
@@ -405,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
             // every MMA issued has completed before the CTAs can release tensor memory
             ptx::mma_commit_pair(drained);
             volatile int never = 0;
-            wait_bar(drained, 0, &never, status, p.wait_limit);
+            wait_bar(drained, 0, &never, status, kWaitLimitCycles);
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
@@ -497,9 +493,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1) mx4_g
     // (the other CTA's MMAs read this one's memory, its warps arrive on this one's barriers)
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 1 && rank == 1) {  // the last arrival of the pair's MMAs on this CTA
-        volatile int never = 0;
-        warp_wait<true>(drained, 0, &never, status, p.wait_limit);
+    volatile int never = 0;
+    if (warp == 1 && rank == 1)  // the last arrival of the pair's MMAs on this CTA
+        warp_wait<true>(drained, 0, &never, status, kWaitLimitCycles);
+    if (tid == 0) {
+        // Every copy issued lands before the CTA can exit (bounded).  A stage's barrier
+        // counts its weights and its rows; where waits have expired one of the two warps
+        // may have asked for stages that the other has not, whose arrival is made here
+        // (as is that of the rows that the test-only stall left out).
+        const int lo = min(s_issued[0], s_issued[1]), hi = max(s_issued[0], s_issued[1]);
+        for (int j = lo; j < hi; ++j) ptx::mbar_arrive(&full[j % kMxStages]);
+        if ((int)blockIdx.x == p.stall_cta && p.stall_stage < s_issued[1])
+            ptx::mbar_arrive(&full[p.stall_stage % kMxStages]);
+        for (int j = max(0, hi - kMxStages); j < hi; ++j)
+            wait_bar(&full[j % kMxStages], (uint32_t)(j / kMxStages) & 1u, &never, status, kWaitLimitCycles);
     }
     __syncwarp();
     ptx::cluster_sync();
@@ -1064,7 +1071,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
         // let every copy issued land before the CTA can exit (bounded)
         volatile int never = 0;
         for (int j = 0; j < NS; ++j)
-            if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, p.wait_limit);
+            if (used >> j & 1) warp_wait(&full[j], (par >> j) & 1, &never, status, kWaitLimitCycles);
     } else if (warp == 1) {
         // --------------------------------------------------------------- MMAs
         const uint32_t issue = ptx::elect_one(), ring_a = ptx::smem_u32(ring), b_a = ptx::smem_u32(s_b);
@@ -1111,7 +1118,7 @@ __global__ void __launch_bounds__(kMdThreads, 1) mx4_decode_kernel(const __grid_
         if (issue) {
             ptx::mma_commit(drained);
             volatile int never = 0;
-            wait_bar(drained, 0, &never, status, p.wait_limit);
+            wait_bar(drained, 0, &never, status, kWaitLimitCycles);
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {

@@ -55,3 +55,71 @@ def test_stalls_of_every_kind_of_stage(T, E, k, n_in, n_out):
                 seen += 1
             _recovers(ws, call, want)
     assert seen >= 4
+
+
+NO_CTA = 1 << 20  # nothing is stalled: only the waits' limit is short
+
+
+def _short_limits(ws, call, want, limits):
+    """The waits of every role run out while what they wait for arrives."""
+    late = 0
+    for us in limits:
+        for _ in range(4):
+            moe.lib().moe_testing_stall(NO_CTA, 0, us)
+            try:
+                out = call()
+                st = moe.get_status(ws)
+            finally:
+                moe.lib().moe_testing_stall(-1, 0, 0)
+            if st == moe.OK:
+                assert torch.equal(out, want)
+            else:
+                assert st == moe.ERR_TIMEOUT
+                late += 1
+        _recovers(ws, call, want)
+    return late
+
+
+# (a wait sleeps up to 20 us before it looks at its limit: long rows make longer waits)
+LIMITS = [1, 2, 5, 10, 15, 20, 21, 22, 23, 24, 25, 30, 35, 40, 60]
+
+
+@pytest.mark.parametrize("T,E,k,n_in,n_out", [(3, 30, 2, 1600, 300), (128, 60, 1, 9216, 2000), (900, 6, 2, 2880, 700),
+                                              (300, 4, 2, 20480, 300), (500, 9, 2, 12288, 1200)])
+def test_waits_that_run_out_while_copies_land(T, E, k, n_in, n_out):
+    W, x, ids = _product(T, E, k, n_in, n_out, T)
+    ws = moe.workspace(T, k, E, n_in)
+
+    def call():
+        return moe.mul_mat_id_mx4(W, E, n_out, n_in, x, ids, ws=ws)
+
+    want = call()
+    assert moe.get_status(ws) == moe.OK
+    late = _short_limits(ws, call, want, LIMITS)
+    assert late > 0 or n_in < 10000
+
+
+@pytest.mark.parametrize("wtype,row", [("q8_0", 34), ("mxfp4", 17)])
+def test_waits_of_the_grouped_gemm_that_run_out(wtype, row):
+    T, E, k, n, ff = 600, 5, 3, 7168, 1024
+    g = torch.Generator().manual_seed(3)
+
+    def weights(n_out, n_in):
+        b = torch.randint(0, 256, (E, n_out, n_in // 32, row), generator=g, dtype=torch.uint8)
+        if wtype == "q8_0":
+            b[..., 0], b[..., 1] = 0, 0x18  # scale 2^-9
+        else:
+            b[..., 0] = 118
+        return moe.weights_prepare(b.cuda(), E, n_out, n_in, wtype=wtype)
+
+    Wg, Wu, Wd = weights(ff, n), weights(ff, n), weights(n, ff)
+    x = torch.randn(T, n, generator=g).bfloat16().cuda()
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int().cuda()
+    ws = moe.workspace(T, k, E, n, ff)
+
+    def call():
+        return moe.ffn(Wg, Wu, Wd, E, n, ff, x, ids, ws=ws, wtype=wtype)[0]
+
+    want = call()
+    assert moe.get_status(ws) == moe.OK
+    assert _short_limits(ws, call, want, LIMITS) > 0
