@@ -40,7 +40,8 @@
  *                by moe_weights_prepare().
  *  - Limits ([PR283] section 2.1, mmq_id.cu#L128-L129, "32-bit packing
  *    safety"): n_tokens < 2^22, k < 2^10; also 1 <= k <= n_experts,
- *    n_tokens*k < 2^31 and n_experts <= 16384.  Violations return
+ *    n_tokens*k + 8*n_experts < 2^31 - 2^14 (positions padded by expert stay
+ *    inside 32 bits) and n_experts <= 16384.  Violations return
  *    MOE_ERR_RANGE.
  */
 #ifndef MOE_H

@@ -15,6 +15,12 @@ namespace moe {
 constexpr int kMaxExperts = 16384;
 constexpr int64_t kMaxTokens = (int64_t)1 << 22;  // exclusive
 constexpr int kMaxK = 1 << 10;                      // exclusive
+// Positions of slots are 32-bit: so are those padded to 8 rows an expert, the rows
+// behind the last one that a copy rounds up to, and a loop's step past the last
+// slot (8192 at most).
+inline bool slots_in_range(int64_t slots, int n_experts) {
+    return slots + 8 * (int64_t)n_experts < ((int64_t)1 << 31) - ((int64_t)1 << 14);
+}
 
 // ------------------------------------------------------- device status word
 // The first error sticks (compare-and-swap from MOE_OK).

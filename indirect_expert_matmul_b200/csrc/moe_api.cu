@@ -28,8 +28,7 @@ static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 static moe_status check_sizes(int64_t n_tokens, int k, int n_experts) {
     if (n_tokens < 0 || k < 1 || n_experts < 1) return MOE_ERR_INVALID;
     if (n_tokens >= kMaxTokens || k >= kMaxK || k > n_experts) return MOE_ERR_RANGE;
-    if (n_tokens * (int64_t)k >= ((int64_t)1 << 31)) return MOE_ERR_RANGE;
-    if (n_experts > kMaxExperts) return MOE_ERR_RANGE;
+    if (n_experts > kMaxExperts || !slots_in_range(n_tokens * (int64_t)k, n_experts)) return MOE_ERR_RANGE;
     return MOE_OK;
 }
 

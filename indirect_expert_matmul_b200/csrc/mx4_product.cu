@@ -1375,7 +1375,7 @@ extern "C" moe_status moe_mul_mat_id_mx4(const void* W_prepared, int n_experts, 
                                          float* dst, void* workspace, moe_stream stream) {
     if (n_tokens < 0 || k < 1 || n_experts < 1) return MOE_ERR_INVALID;
     if (n_tokens >= kMaxTokens || k >= kMaxK || k > n_experts) return MOE_ERR_RANGE;
-    if (n_tokens * (int64_t)k >= ((int64_t)1 << 31) || n_experts > kMaxExperts) return MOE_ERR_RANGE;
+    if (n_experts > kMaxExperts || !slots_in_range(n_tokens * (int64_t)k, n_experts)) return MOE_ERR_RANGE;
     if (mode != MOE_BROADCAST && mode != MOE_PER_SLOT) return MOE_ERR_INVALID;
     if (x_type != MOE_BF16 && x_type != MOE_F16 && x_type != MOE_F32) return MOE_ERR_INVALID;
     if (n_out <= 0 || n_in <= 0 || n_in % 32) return MOE_ERR_INVALID;

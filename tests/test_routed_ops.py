@@ -171,3 +171,18 @@ def test_reference_gradient_by_differences():
                     a[t, e] += h
                     b[t, e] -= h
                     assert abs((loss(a) - loss(b)) / (2 * h) - d[t, e]) < 1e-8
+
+
+def test_slots_that_leave_32_bits_on_the_way_are_refused():
+    # 2147483136 and a little fewer slots: positions padded by expert, or stepped past the last slot, pass 2^31
+    L, nul = moe.lib(), None
+    T = (1 << 22) - 1
+    for k, E, tokens in ((512, 512, T), (512, 1024, T), (512, 512, T - 16), (1023, 1023, (1 << 31) // 1023)):
+        assert tokens * k < 1 << 31
+        assert L.moe_row_ids(nul, tokens, k, E, 0, nul, nul, nul, nul, nul) == moe.ERR_RANGE
+        assert L.moe_mul_mat_id(nul, E, 8, 64, nul, 0, nul, tokens, k, 0, nul, nul, nul) == moe.ERR_RANGE
+        assert L.moe_ffn(nul, nul, nul, E, 64, 64, nul, nul, nul, 0, nul, 0, nul, tokens, k, nul, nul, nul,
+                         nul) == moe.ERR_RANGE
+        assert L.moe_mul_mat_id_mx4(nul, E, 8, 64, nul, 0, nul, tokens, k, 0, nul, nul, nul) == moe.ERR_RANGE
+    assert L.moe_row_ids(nul, T, 511, 1024, 0, nul, nul, nul, nul, nul) == moe.ERR_INVALID  # (null pointers)
+    assert L.moe_mul_mat_id_mx4(nul, 1024, 8, 64, nul, 0, nul, T, 511, 0, nul, nul, nul) == moe.ERR_INVALID
