@@ -116,7 +116,8 @@ struct WsLayout {
         h_sh = o; o += up(hs_gemv > hs_gemm ? hs_gemv : hs_gemm);
         xt = o; o += up((size_t)rows_pad * kin * 128);
         xt_sh = o; o += n_hidden_sh > 0 ? up((size_t)rows_pad_sh * kin * 128) : 0;
-        xs = o; o += up((size_t)rows_pad * 8);  // power-of-two scale of each tiled activation row (4-bit: scale bytes)
+        // power-of-two scale of each tiled activation row (n_in <= 64: or the 4-bit product's 8 scale bytes)
+        xs = o; o += up((size_t)rows_pad * (n_in <= kTileK ? 8 : 4));
         xs_sh = o; o += n_hidden_sh > 0 ? up((size_t)rows_pad_sh * 4) : 0;
         total = o;
     }

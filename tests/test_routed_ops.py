@@ -186,3 +186,19 @@ def test_slots_that_leave_32_bits_on_the_way_are_refused():
         assert L.moe_mul_mat_id_mx4(nul, E, 8, 64, nul, 0, nul, tokens, k, 0, nul, nul, nul) == moe.ERR_RANGE
     assert L.moe_row_ids(nul, T, 511, 1024, 0, nul, nul, nul, nul, nul) == moe.ERR_INVALID  # (null pointers)
     assert L.moe_mul_mat_id_mx4(nul, 1024, 8, 64, nul, 0, nul, T, 511, 0, nul, nul, nul) == moe.ERR_INVALID
+
+
+@pytest.mark.parametrize("n_in", [32, 64, 96, 7168])
+def test_workspace_holds_what_the_products_use(n_in):
+    # header, slot and expert tables, 16-bit rows by 64 values, and a factor a row (for up to 64 values the
+    # 4-bit product's 8 scale bytes take its place; beyond, they lie behind its codes)
+    T, k, E = 4096, 8, 256
+    up = lambda v: (v + 255) // 256 * 256
+    rows = T * k + 8 * E + 32
+    size = 256 + 3 * up(T * k * 4) + 4 * up((E + 1) * 4) + up((2 * 64 * E + E) * 4)
+    size += up(rows * ((n_in + 63) // 64) * 128)
+    size += up(rows * (8 if n_in <= 64 else 4))
+    assert moe.workspace_size(T, k, E, n_in) == size
+    planes, scale_rows = (n_in + 255) // 256, (rows + 3) // 4 * 4
+    if n_in > 64:
+        assert planes * (rows * 128 + scale_rows * 8) <= rows * ((n_in + 63) // 64) * 128
