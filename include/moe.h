@@ -271,7 +271,9 @@ MOE_API moe_status moe_ffn_decode_noalloc(const void *Wg, const void *Wu, const 
  * The indirect product with both operands in MXFP4: x is rounded to MXFP4
  * blocks along n_in exactly as moe_mxfp4_quantize rounds, and
  *   dst[t][s][:] = W[ids[t][s]] . Q(x[r]),   r = t (broadcast) or (t, s) (per_slot).
- * Products of the rounded operands are exact; sums are float.  A block of x
+ * Products of the rounded operands are exact; sums are float, within
+ * (n_in / 8 + 8) * 2^-24 of the terms' magnitudes and exact where float holds
+ * every partial sum.  A block of x
  * that holds a NaN or an infinity makes its token's results NaN.  W_prepared
  * comes from moe_weights_prepare_w(MOE_MXFP4, ...); layouts, limits, errors and
  * the workspace (moe_workspace_size with n_hidden = 0) are those of
