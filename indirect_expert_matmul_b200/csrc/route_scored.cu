@@ -169,7 +169,7 @@ struct Key {
         const double hi = __dadd_rn(h, r), rr = __dsub_rn(hi, h);
         const double lo = __dadd_rn(__dsub_rn(h, __dsub_rn(hi, rr)), __dsub_rn(r, rr));
         if (fabs(hi) < INFINITY) return {hi, lo};
-        return {h == h ? h : -INFINITY, 0.0};  // an infinite bias; NaN counts as the lowest
+        return {fabs(h) == INFINITY && c == c ? h : -INFINITY, 0.0};  // an infinite bias; NaN counts as the lowest
     }
     __device__ bool operator>(const Key& o) const { return hi > o.hi || (hi == o.hi && lo > o.lo); }
     __device__ bool operator==(const Key& o) const { return hi == o.hi && lo == o.lo; }

@@ -113,3 +113,20 @@ def test_reordered_choices_of_many_tokens(E, k):
     ids, _ = moe.route_scored(l, k, bias=b.cuda())
     key = 0.5 * torch.tanh(0.5 * l.double()) + b.double().cuda()  # (1/2 less: exact to 1e-17)
     assert torch.equal(ids.long(), torch.sort(key, dim=1, descending=True, stable=True).indices[:, :k])
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_a_nan_among_close_keys_stays_last(score):
+    # as many experts as are left without it, close to one another: put in order by their 64-bit keys
+    for E, k in ((20, 19), (64, 63), (96, 8)):
+        l = torch.zeros(4, E)
+        l[:, 5] = float("nan")
+        l = l.cuda()
+        b = torch.full((E,), 0.25)
+        b[5] = 2.0
+        if score == "sigmoid":
+            ids, _ = moe.route_scored(l, k, bias=b.cuda())
+            assert (ids == torch.tensor([e for e in range(E) if e != 5][:k], dtype=torch.int32).cuda()).all()
+        else:  # every score is NaN: any k experts
+            ids, _ = moe.route_scored(l, k, bias=b.cuda(), score=score)
+            assert all(len(set(r)) == k and 0 <= min(r) and max(r) < E for r in ids.tolist())
