@@ -186,6 +186,7 @@ struct Exact {
     float mx;     // softmax: the largest logit
     double* key;  // [n_experts]: the keys' hi
     double z;     // softmax: the denominator
+    bool rests;   // whether any key's lo, or what a group score's hi lacks, is not 0 (after fill)
 
     __device__ void denominator(int lane) {
         if (!p.softmax || z != 0.0) return;
@@ -222,8 +223,14 @@ struct Exact {
     }
     __device__ void fill(int lane) {
         denominator(lane);
+        bool rest = false;
 #pragma unroll 1
-        for (int e = lane; e < p.n_experts; e += 32) key[e] = key_of(e).hi;
+        for (int e = lane; e < p.n_experts; e += 32) {
+            const Key k = key_of(e);
+            key[e] = k.hi;
+            rest = rest || k.lo != 0.0;
+        }
+        rests = __any_sync(0xffffffffu, rest);
         __syncwarp();
     }
     // Whether expert e with the high part v comes before f with w (kNone: no
@@ -231,14 +238,15 @@ struct Exact {
     static constexpr int kNone = 0x7fffffff;
     __device__ bool before(double v, int e, double w, int f) const {
         if (v != w || e == kNone || f == kNone) return e != kNone && (f == kNone || v > w);
+        if (!rests) return e < f;
         const float l = load_logit(p.logits, p.type, row + e), o = load_logit(p.logits, p.type, row + f);
         if (l == o && (!p.bias || __ldg(p.bias + e) == __ldg(p.bias + f))) return e < f;
         const double a = key_of(e).lo, b = key_of(f).lo;
         return a > b || (a == b && e < f);
     }
     // Lane g: the score of group g as one double; mag: the largest magnitude of terms.
-    __device__ double group_score(int lane, int size, double& mag) const {
-        double mine = -INFINITY;
+    __device__ double group_score(int lane, int size, double& mag) {
+        Key mine = {-INFINITY, 0.0};  // its two largest, then their sum
         mag = 0.0;
 #pragma unroll 1
         for (int g = 0; g < p.n_groups; ++g) {
@@ -257,9 +265,13 @@ struct Exact {
             }
             const double terms = p.group_top == 2 ? fabs(a) + fabs(b) : fabs(a);
             if (terms < INFINITY) mag = fmax(mag, terms);
-            if (lane == g) mine = p.group_top == 2 ? a + b : a;
+            if (lane == g) mine = {a, b};
         }
-        return mine;
+        if (p.group_top == 2) {
+            mine = Key::sum(mine.hi, mine.lo, 0.0);
+            rests = __any_sync(0xffffffffu, rests || mine.lo != 0.0);
+        }
+        return mine.hi;
     }
     // The same with the rests (~2 us a token, for groups that the doubles leave close).
     __device__ Key group_key(int lane, int size) const {
@@ -351,9 +363,9 @@ __device__ __forceinline__ void group_top2(const F& value, int lane, int E, int 
 }
 
 // (registers: the double-precision side would take up to 72 everywhere; held to
-// what the float side needs, it spills: 8191 x 128 softmax without a bias 7.1 us for 7.4)
+// what the float side needs, it spills: 8191 x 128 softmax without a bias 7.0 us for 7.4)
 template <int NPL, bool BIAS>
-__global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 10 : NPL == 8 ? 8 : 1) route_scored_kernel(const RouteScoredArgs p) {
+__global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : NPL == 8 ? 8 : 1) route_scored_kernel(const RouteScoredArgs p) {
     __shared__ double s_key[kRsWarps][32 * NPL];
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * kRsWarps + (threadIdx.x >> 5);
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 10 :
 #pragma unroll
         for (int j = 0; j < NPL; ++j) s[j] = __fdividef(1.f, 1.f + __expf(-l[j]));
     }
-    Exact exact64 = {p, t * p.ld, mx, s_key[threadIdx.x >> 5], 0.0};
+    Exact exact64 = {p, t * p.ld, mx, s_key[threadIdx.x >> 5], 0.0, true};
     const int size = E / p.n_groups;
     uint32_t open = 0xffffffffu;  // bit g: group g
     // keys; 0: not available (past the row's end, later: chosen or in a closed group)
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 10 :
                 // (roundings of the terms, 2^-53 each, and of their sum)
                 const bool near = lane < G && rank == p.topk_groups - 1 && next > -INFINITY &&
                                   best - next <= 0x1p-50 * (1.0 + mag64);
-                if (__any_sync(0xffffffffu, near)) {
+                if (__any_sync(0xffffffffu, near) && exact64.rests) {
                     const Key full = exact64.group_key(lane, size);
                     rank = 0;
                     for (int g = 0; g < G; ++g) {
