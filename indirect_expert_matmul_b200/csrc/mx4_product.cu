@@ -28,11 +28,11 @@
 // MMAs, one warp finds the units, four scatter the accumulators to dst.
 //
 // What bounds it: the gate product (256 experts, 4096 tokens top-8, 7168 -> 2048:
-// 2.0 GB of weights, 0.27 of results, 0.12 of rounded rows) takes 381 us, 6.3 TB/s
-// where a copy reaches 6.46, and 440 where the power limit holds the SM clock at
+// 2.0 GB of weights, 0.27 of results, 0.12 of rounded rows) takes 377 us, 6.4 TB/s
+// where a copy reaches 6.46, and 419 to 440 where the power limit holds the SM clock at
 // 1.3 GHz.  A product whose experts' weights are read again from L2 (128 experts,
-// 8192 tokens top-4, 2880 -> 2880: 223 us) is bound by the way of a stage through
-// copies, scales and MMAs, 7 in flight: ~750 cycles a stage, of which ~260 are
+// 8192 tokens top-4, 2880 -> 2880: 229 us, 259 in long runs) is bound by the way of a
+// stage through copies, scales and MMAs, 7 in flight: ~770 cycles a stage, of which ~260 are
 // MMAs; DRAM is at half its rate.  Weights asked into L2 ahead (by bulk prefetches
 // or by a warp's) made both slower: 274 and 426 us.
 #include <cuda.h>
@@ -666,9 +666,10 @@ mx4_gather_kernel(const void* __restrict__ x, int n_in, const int32_t* __restric
 // stable counting sort - and rounds its rows straight into their tile rows.
 // Up to kMpSelfSlots slots every CTA reads all the ids.  Beyond, a launch before
 // counts the chunk of kMpParts CTAs and a CTA sums the chunks' counts and counts
-// its chunk's slots before its own.  (The whole call
-// for 512 slots, 256 experts, 2048 -> 512: 42 us by itself, 46 with the launch
-// before, which pays where a CTA would count many more.)
+// its chunk's slots before its own.  The whole call for 256 experts, top-8, 512 ->
+// 128, by itself / with the launch before, us: 20.8 / 25.8 at 8192 slots, 27.8 / 30.5
+// at 32768, 42.3 / 41.9 at 65536, 69.8 / 61.8 at 131072; 25.8 / 28.4 and 37.6 / 36.8
+// where one expert takes all 32768 or 65536 (8 experts, top-2: 29.3 / 30.3 and 44.0 / 42.6).
 constexpr int kMpThreads = 1024;
 constexpr int kMpMaxCtas = 148, kMpParts = 4;
 constexpr int64_t kMpSelfSlots = 32768;
@@ -759,12 +760,12 @@ __global__ void __launch_bounds__(kMpThreads) mx4_place_kernel(const MxPlaceArgs
         bad |= count_slots(p.ids, (int)(t0 * k), (int)(p.T * k), E, s_row);
         if (bad) set_status(p.hdr + kHdrStatus, MOE_ERR_BAD_ID);
         if (__syncthreads_or(bad || stop)) return;
-            if (tid < E) all = s_base[tid] + s_row[tid];
+        if (tid < E) all = s_base[tid] + s_row[tid];
         __syncthreads();
     } else {
         const int chunk = g / kMpParts, C = (G + kMpParts - 1) / kMpParts;
         count_slots(p.ids, (int)(mp_token(p.T, chunk * kMpParts, G) * k), (int)(t0 * k), E, s_base);
-            if (__syncthreads_or(tid == 0 && read_status(p.hdr + kHdrStatus) != 0)) return;
+        if (__syncthreads_or(tid == 0 && read_status(p.hdr + kHdrStatus) != 0)) return;
         // 1024 / E threads an expert, each some of the chunks
         const int Ep = (E + 31) & ~31, parts = kMpThreads / Ep;
         const int e = tid % Ep, part = tid / Ep;
@@ -1318,9 +1319,10 @@ bool plan_weights(Mx4Params& p, int n_experts, int stage_kt) {
 }
 
 // An ordinary launch: no kernel here starts before its stream's previous one has
-// ended.  (Launched as programmatic dependents, the next kernel's blocks set up
-// meanwhile, calls on three streams at once came to a standstill after some hundred
-// thousand; no block holds an SM, or its tensor memory, waiting for another grid.)
+// ended.  (As programmatic dependents, whose blocks set up and took tensor memory
+// before that, calls on three streams at once came to a standstill after some
+// hundred thousand.  The cause was not found; with ordinary launches no block holds
+// an SM, or its tensor memory, waiting for another grid.)
 template <typename A>
 moe_status launch(void (*kernel)(A), unsigned grid, int threads, size_t smem, cudaStream_t stream, const A& args) {
     kernel<<<grid, threads, smem, stream>>>(args);
