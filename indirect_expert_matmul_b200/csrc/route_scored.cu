@@ -30,6 +30,8 @@ namespace moe {
 namespace {
 
 constexpr int kRsWarps = 4;
+template <int NPL, bool BIAS>
+constexpr int kRsCtaWarps = BIAS && NPL == 32 ? 2 : kRsWarps;  // (16 bytes an expert and warp of shared memory)
 constexpr int kRsMaxPerLane = 32;  // n_experts <= 1024
 constexpr int kRsMaxGroups = 32;
 constexpr int64_t kRsHalfTokens = 148 * 32;  // above: a scheduler has more than 8 tokens
@@ -179,14 +181,18 @@ struct Key {
 // time: kept in registers and unrolled over the lane's experts it took so many
 // that the 4096-token prompt of 256 experts ran in 29 us.  A score is worked out
 // as its distance from 0, 1/2 or 1 (softmax: from 0 or the largest score), so
-// that scores which round to one double, a sigmoid's above 37 to 1, keep their order.
+// that scores which round to one double, a sigmoid's above 37 to 1, keep their
+// order: keys are a double and what it lacks, both in shared memory (worked out
+// again where two doubles are equal, it took 7 us more in a cold instruction cache).
+// Without a bias keys order like logits, which stand for the rests.
+template <bool BIAS>
 struct Exact {
     const RouteScoredArgs& p;
     int64_t row;
     float mx;     // softmax: the largest logit
-    double* key;  // [n_experts]: the keys' hi
+    double* key;   // [n_experts]: the keys' hi
+    double* rest;  // [n_experts]: their lo (with a bias)
     double z;     // softmax: the denominator
-    bool rests;   // whether any key's lo, or what a group score's hi lacks, is not 0 (after fill)
 
     __device__ void denominator(int lane) {
         if (!p.softmax || z != 0.0) return;
@@ -200,8 +206,8 @@ struct Exact {
     }
     __device__ Key key_of(int e) const {
         const float l = load_logit(p.logits, p.type, row + e);
-        const double b = p.bias ? (double)__ldg(p.bias + e) : 0.0;
-        double base = 0.0, rest = 0.0;
+        const double b = BIAS ? (double)__ldg(p.bias + e) : 0.0;
+        double base = 0.0, far = 0.0;
         if (l != -INFINITY) {
             // r = exp of -|l| or of l - mx, m = r - 1 without its cancellation
             const double x = p.softmax ? (double)l - (double)mx : -fabs((double)l), r = exp(x);
@@ -209,28 +215,26 @@ struct Exact {
             const double big = 1.0 / (p.softmax ? z : 1.0 + r);
             if (p.softmax) {
                 base = x > -0.5 ? big : 0.0;
-                rest = big * (x > -0.5 ? m : r);
+                far = big * (x > -0.5 ? m : r);
             } else if (x > -1.0) {  // 1 / (1 + exp(-l)) - 1/2 = (1 - exp(-|l|)) / (1 + exp(-|l|)) / 2, signed
                 base = 0.5;
-                rest = copysign(0.5 * m * big, (double)l);
+                far = copysign(0.5 * m * big, (double)l);
             } else {
                 base = l > 0.f ? 1.0 : 0.0;
-                rest = r * big;
-                if (l > 0.f) rest = -rest;
+                far = r * big;
+                if (l > 0.f) far = -far;
             }
         }
-        return Key::sum(base, b, rest);
+        return Key::sum(base, b, far);
     }
     __device__ void fill(int lane) {
         denominator(lane);
-        bool rest = false;
 #pragma unroll 1
         for (int e = lane; e < p.n_experts; e += 32) {
             const Key k = key_of(e);
             key[e] = k.hi;
-            rest = rest || k.lo != 0.0;
+            if (BIAS) rest[e] = k.lo;
         }
-        rests = __any_sync(0xffffffffu, rest);
         __syncwarp();
     }
     // Whether expert e with the high part v comes before f with w (kNone: no
@@ -238,74 +242,48 @@ struct Exact {
     static constexpr int kNone = 0x7fffffff;
     __device__ bool before(double v, int e, double w, int f) const {
         if (v != w || e == kNone || f == kNone) return e != kNone && (f == kNone || v > w);
-        if (!rests) return e < f;
-        const float l = load_logit(p.logits, p.type, row + e), o = load_logit(p.logits, p.type, row + f);
-        if (l == o && (!p.bias || __ldg(p.bias + e) == __ldg(p.bias + f))) return e < f;
-        const double a = key_of(e).lo, b = key_of(f).lo;
+        const double a = BIAS ? rest[e] : load_logit(p.logits, p.type, row + e);
+        const double b = BIAS ? rest[f] : load_logit(p.logits, p.type, row + f);
         return a > b || (a == b && e < f);
     }
-    // Lane g: the score of group g as one double; mag: the largest magnitude of terms.
-    __device__ double group_score(int lane, int size, double& mag) {
-        Key mine = {-INFINITY, 0.0};  // its two largest, then their sum
-        mag = 0.0;
-#pragma unroll 1
-        for (int g = 0; g < p.n_groups; ++g) {
-            double a = -INFINITY, b = -INFINITY;
-#pragma unroll 1
-            for (int e = g * size + lane; e < (g + 1) * size; e += 32) {
-                const double v = key[e];
-                b = fmax(b, fmin(a, v));
-                a = fmax(a, v);
+    // Lane g: the score of group g, each group scanned by as many lanes as there are for it
+    // (one group after the other by the whole warp took 2 us a token).
+    __device__ Key group_score(int lane, int size) const {
+        int P = 1;
+        while (2 * P * p.n_groups <= 32) P *= 2;
+        const int g = lane / P, end = g < p.n_groups ? (g + 1) * size : 0;
+        double a = -INFINITY, b = -INFINITY;  // the group's two first, ea and eb
+        int ea = kNone, eb = kNone;
+        auto take = [&](double v, int e) {
+            if (before(v, e, a, ea)) {
+                b = a; eb = ea;
+                a = v; ea = e;
+            } else if (before(v, e, b, eb)) {
+                b = v; eb = e;
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const double oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-                b = fmax(fmax(b, ob), fmin(a, oa));
-                a = fmax(a, oa);
-            }
-            const double terms = p.group_top == 2 ? fabs(a) + fabs(b) : fabs(a);
-            if (terms < INFINITY) mag = fmax(mag, terms);
-            if (lane == g) mine = {a, b};
+        };
+#pragma unroll 1
+        for (int e = g * size + lane % P; e < end; e += P) take(key[e], e);
+        __syncwarp();
+#pragma unroll 1
+        for (int o = 1; o < P; o <<= 1) {
+            const double oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
+            const int oea = __shfl_xor_sync(0xffffffffu, ea, o), oeb = __shfl_xor_sync(0xffffffffu, eb, o);
+            take(oa, oea);
+            take(ob, oeb);
+            __syncwarp();
         }
-        if (p.group_top == 2) {
-            mine = Key::sum(mine.hi, mine.lo, 0.0);
-            rests = __any_sync(0xffffffffu, rests || mine.lo != 0.0);
+        double lo = 0.0;
+#pragma unroll 1
+        for (int j = 0; j < p.group_top; ++j) {
+            const int e = j ? eb : ea;
+            if (e != kNone) lo += BIAS ? rest[e] : key_of(e).lo;
         }
-        return mine.hi;
-    }
-    // The same with the rests (~2 us a token, for groups that the doubles leave close).
-    __device__ Key group_key(int lane, int size) const {
-        Key mine = {-INFINITY, 0.0};
-#pragma unroll 1
-        for (int g = 0; g < p.n_groups; ++g) {
-            double a = -INFINITY, b = -INFINITY;  // the group's two first, ea and eb
-            int ea = kNone, eb = kNone;
-            auto take = [&](double v, int e) {
-                if (before(v, e, a, ea)) {
-                    b = a; eb = ea;
-                    a = v; ea = e;
-                } else if (before(v, e, b, eb)) {
-                    b = v; eb = e;
-                }
-            };
-#pragma unroll 1
-            for (int e = g * size + lane; e < (g + 1) * size; e += 32) take(key[e], e);
-#pragma unroll 1
-            for (int o = 16; o > 0; o >>= 1) {
-                const double oa = __shfl_xor_sync(0xffffffffu, a, o), ob = __shfl_xor_sync(0xffffffffu, b, o);
-                const int oea = __shfl_xor_sync(0xffffffffu, ea, o), oeb = __shfl_xor_sync(0xffffffffu, eb, o);
-                take(oa, oea);
-                take(ob, oeb);
-            }
-            if (lane == g) {
-                mine = key_of(ea);
-                if (p.group_top == 2) {
-                    const Key second = key_of(eb);
-                    mine = Key::sum(mine.hi, second.hi, __dadd_rn(mine.lo, second.lo));
-                }
-            }
-        }
-        return mine;
+        __syncwarp();
+        const Key k = Key::sum(a, p.group_top == 2 ? b : 0.0, lo);
+        const int from = lane < p.n_groups ? lane * P : 0;
+        const Key mine = {__shfl_sync(0xffffffffu, k.hi, from), __shfl_sync(0xffffffffu, k.lo, from)};
+        return lane < p.n_groups ? mine : Key{-INFINITY, 0.0};
     }
     // The k largest keys of open groups (equal: lower expert) to ids.
     __device__ void choose(int lane, int size, uint32_t open, int32_t* ids) const {
@@ -362,13 +340,14 @@ __device__ __forceinline__ void group_top2(const F& value, int lane, int E, int 
     }
 }
 
-// (registers: the double-precision side would take up to 72 everywhere; held to
-// what the float side needs, it spills: 8191 x 128 softmax without a bias 7.0 us for 7.4)
+// (registers held to what the float side needs: where the double-precision side set
+// them, 8191 x 128 softmax without a bias took 7.4 us for 7.0)
 template <int NPL, bool BIAS>
-__global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : NPL == 8 ? 8 : 1) route_scored_kernel(const RouteScoredArgs p) {
-    __shared__ double s_key[kRsWarps][32 * NPL];
+__global__ void __launch_bounds__(kRsCtaWarps<NPL, BIAS> * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : NPL == 8 ? 8 : 1) route_scored_kernel(const RouteScoredArgs p) {
+    constexpr int kWarps = kRsCtaWarps<NPL, BIAS>;
+    __shared__ double s_key[kWarps][32 * NPL], s_rest[BIAS ? kWarps : 1][BIAS ? 32 * NPL : 1];
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kRsWarps + (threadIdx.x >> 5);
+    const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= p.n_tokens) return;
     const int E = p.n_experts, e0 = lane * NPL;
     const bool softmax = p.softmax, grouped = p.topk_groups < p.n_groups;
@@ -405,7 +384,7 @@ __global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : 
 #pragma unroll
         for (int j = 0; j < NPL; ++j) s[j] = __fdividef(1.f, 1.f + __expf(-l[j]));
     }
-    Exact exact64 = {p, t * p.ld, mx, s_key[threadIdx.x >> 5], 0.0, true};
+    Exact<BIAS> exact64 = {p, t * p.ld, mx, s_key[threadIdx.x >> 5], s_rest[BIAS ? threadIdx.x >> 5 : 0], 0.0};
     const int size = E / p.n_groups;
     uint32_t open = 0xffffffffu;  // bit g: group g
     // keys; 0: not available (past the row's end, later: chosen or in a closed group)
@@ -465,26 +444,11 @@ __global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : 
             const float terms = 1.2e-7f * __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(own)));
             if (hi >= rival(lo, 2.f * err + terms) && lo > ordered(-INFINITY)) {
                 exact64.fill(lane);
-                double mag64;
-                const double best = exact64.group_score(lane, size, mag64);
+                const Key best = exact64.group_score(lane, size);
                 rank = 0;
-                double next = -INFINITY;  // the best score that is not ahead of this lane's
                 for (int g = 0; g < G; ++g) {
-                    const double o = __shfl_sync(0xffffffffu, best, g);
-                    const bool ahead = o > best || (o == best && g < lane);
-                    rank += ahead;
-                    if (!ahead && g != lane) next = fmax(next, o);
-                }
-                // (roundings of the terms, 2^-53 each, and of their sum)
-                const bool near = lane < G && rank == p.topk_groups - 1 && next > -INFINITY &&
-                                  best - next <= 0x1p-50 * (1.0 + mag64);
-                if (__any_sync(0xffffffffu, near) && exact64.rests) {
-                    const Key full = exact64.group_key(lane, size);
-                    rank = 0;
-                    for (int g = 0; g < G; ++g) {
-                        const Key o = {__shfl_sync(0xffffffffu, full.hi, g), __shfl_sync(0xffffffffu, full.lo, g)};
-                        rank += o > full || (o == full && g < lane);
-                    }
+                    const Key o = {__shfl_sync(0xffffffffu, best.hi, g), __shfl_sync(0xffffffffu, best.lo, g)};
+                    rank += o > best || (o == best && g < lane);
                 }
                 in = lane < G && rank < p.topk_groups;
             }
@@ -615,9 +579,10 @@ __global__ void __launch_bounds__(kRsWarps * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : 
 
 template <int NPL>
 void launch_fwd(const RouteScoredArgs& a, cudaStream_t s) {
-    const unsigned blocks = (unsigned)((a.n_tokens + kRsWarps - 1) / kRsWarps);
-    if (a.bias) route_scored_kernel<NPL, true><<<blocks, kRsWarps * 32, 0, s>>>(a);
-    else route_scored_kernel<NPL, false><<<blocks, kRsWarps * 32, 0, s>>>(a);
+    auto grid = [&](int warps) { return (unsigned)((a.n_tokens + warps - 1) / warps); };
+    constexpr int kBiased = kRsCtaWarps<NPL, true>, kPlain = kRsCtaWarps<NPL, false>;
+    if (a.bias) route_scored_kernel<NPL, true><<<grid(kBiased), kBiased * 32, 0, s>>>(a);
+    else route_scored_kernel<NPL, false><<<grid(kPlain), kPlain * 32, 0, s>>>(a);
 }
 
 struct RouteScoredBwdArgs {
