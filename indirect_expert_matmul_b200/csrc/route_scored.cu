@@ -13,8 +13,9 @@
 // The choice is that of the rule over real numbers.  Float keys carry a bound on
 // their error; wherever two of them are closer than that, the candidates (or
 // the groups) are compared again in double, so that the choice does not depend
-// on how a float was rounded, nor on a score that rounds to 0, 1/2 or 1.  Without a bias the order of the scores is that
-// of the logits, which are compared as they are.
+// on how a float was rounded, nor on a score that rounds to 0, 1/2 or 1.  Without
+// a bias the order of the scores is that of the logits, which are compared as
+// they are.
 //
 // One warp per token, NPL consecutive experts a lane (E <= 32 NPL), read once
 // with 16-byte loads.  A round of the choice is one warp-wide maximum of the
@@ -189,10 +190,10 @@ template <bool BIAS>
 struct Exact {
     const RouteScoredArgs& p;
     int64_t row;
-    float mx;     // softmax: the largest logit
+    float mx;      // softmax: the largest logit
     double* key;   // [n_experts]: the keys' hi
     double* rest;  // [n_experts]: their lo (with a bias)
-    double z;     // softmax: the denominator
+    double z;      // softmax: the denominator
 
     __device__ void denominator(int lane) {
         if (!p.softmax || z != 0.0) return;
@@ -343,7 +344,8 @@ __device__ __forceinline__ void group_top2(const F& value, int lane, int E, int 
 // (registers held to what the float side needs: where the double-precision side set
 // them, 8191 x 128 softmax without a bias took 7.4 us for 7.0)
 template <int NPL, bool BIAS>
-__global__ void __launch_bounds__(kRsCtaWarps<NPL, BIAS> * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : NPL == 8 ? 8 : 1) route_scored_kernel(const RouteScoredArgs p) {
+__global__ void __launch_bounds__(kRsCtaWarps<NPL, BIAS> * 32, NPL <= 2 ? 12 : NPL == 4 ? 9 : NPL == 8 ? 8 : 1)
+route_scored_kernel(const RouteScoredArgs p) {
     constexpr int kWarps = kRsCtaWarps<NPL, BIAS>;
     __shared__ double s_key[kWarps][32 * NPL], s_rest[BIAS ? kWarps : 1][BIAS ? 32 * NPL : 1];
     const int lane = threadIdx.x & 31;
