@@ -19,7 +19,8 @@
  *    of ids, so the host-buffer lifetime hazard discussed in [PR283] section 5
  *    (ids_host / rmapping leaving scope before an async copy) cannot arise.
  *  - All work is enqueued on `stream` (a cudaStream_t; NULL = legacy default
- *    stream) and returns without synchronising.  Argument errors found on the
+ *    stream) and returns without synchronising.  The device of the stream and
+ *    of every pointer is the calling thread's current one.  Argument errors found on the
  *    host return a negative moe_status at once and enqueue nothing.
  *  - Errors found on the device (an id outside [0, n_experts), a bounded wait
  *    that expired) are written to a status word inside the caller's

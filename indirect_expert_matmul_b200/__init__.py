@@ -116,10 +116,6 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(device=None):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
 _XTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
 _MODE = {"broadcast": BROADCAST, "per_slot": PER_SLOT, BROADCAST: BROADCAST, PER_SLOT: PER_SLOT}
 
@@ -158,15 +154,20 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _call(what, dev, fn, *args):
-    """Run an entry point with `dev` current and its current stream as the last
-    argument (a launch needs its stream's device to be the current one)."""
+def _on(dev, fn, *args):
+    """An entry point's status, called with `dev` current and its current stream
+    as the last argument (a launch needs its stream's device to be the current
+    one, and a default stream's handle is the same on every device)."""
     i = dev.index
     if i == torch.cuda.current_device():
-        rc = fn(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(i))
+        return fn(*args, _raw_stream(i))
+    with torch.cuda.device(dev):
+        return fn(*args, _raw_stream(i))
+
+
+def _call(what, dev, fn, *args):
+    """Run an entry point as _on does; MoeError unless it returns OK."""
+    rc = _on(dev, fn, *args)
     if rc != OK:
         raise MoeError(rc, what)
 
@@ -207,13 +208,13 @@ def workspace(n_tokens, k, n_experts, n_in, n_hidden=0, n_hidden_shared=0, x_dty
     """A zero-status workspace tensor (uint8) for calls of these sizes."""
     n = workspace_size(n_tokens, k, n_experts, n_in, n_hidden, n_hidden_shared, x_dtype)
     ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
-    _chk(_L().moe_workspace_init(_ptr(ws), _stream(ws.device)), "moe_workspace_init")
+    _call("moe_workspace_init", ws.device, _L().moe_workspace_init, _ptr(ws))
     return ws
 
 
 def get_status(ws) -> int:
-    """Synchronise the current stream, return and clear the device status."""
-    return _L().moe_get_status(_ptr(ws), _stream(ws.device))
+    """Synchronise the current stream of ws's device, return and clear the device status."""
+    return _on(ws.device, _L().moe_get_status, _ptr(ws))
 
 
 # ---------------------------------------------------------------- weights
@@ -233,8 +234,8 @@ def weights_prepare(blocks, n_experts, n_out, n_in, out=None, wtype="q8_0"):
     if out is None:
         out = torch.empty(n, dtype=torch.uint8, device=blocks.device)
     _need(out, "out", torch.uint8, n, blocks.device)
-    _chk(_L().moe_weights_prepare_w(w, _ptr(blocks), n_experts, n_out, n_in, _ptr(out), _stream(blocks.device)),
-         "moe_weights_prepare")
+    _call("moe_weights_prepare", blocks.device, _L().moe_weights_prepare_w, w, _ptr(blocks), n_experts, n_out, n_in,
+          _ptr(out))
     return out
 
 
@@ -276,8 +277,8 @@ def row_ids(ids, n_experts, mode="broadcast", ws=None):
     if ws is None:
         ws = workspace(T, k, n_experts, 0, device=dev)
     _need(ws, "ws", torch.uint8, workspace_size(T, k, n_experts, 0), dev)
-    _chk(_L().moe_row_ids(_ptr(ids), T, k, n_experts, _MODE[mode], _ptr(src1), _ptr(dst), _ptr(bounds), _ptr(ws),
-                          _stream(dev)), "moe_row_ids")
+    _call("moe_row_ids", dev, _L().moe_row_ids, _ptr(ids), T, k, n_experts, _MODE[mode], _ptr(src1), _ptr(dst),
+          _ptr(bounds), _ptr(ws))
     return src1[:S], dst[:S], bounds
 
 
@@ -302,8 +303,8 @@ def mul_mat_id(W, n_experts, n_out, n_in, x, ids, mode="broadcast", ws=None, out
     if out is None:
         out = torch.empty((T, k, n_out), dtype=torch.float32, device=dev)
     _need(out, "out", torch.float32, T * k * n_out, dev)
-    _chk(_L().moe_mul_mat_id_w(w, _ptr(W), n_experts, n_out, n_in, _ptr(x), _XTYPE[x.dtype], _ptr(ids), T, k,
-                               _MODE[mode], _ptr(out), _ptr(ws), _stream(x.device)), "moe_mul_mat_id")
+    _call("moe_mul_mat_id", dev, _L().moe_mul_mat_id_w, w, _ptr(W), n_experts, n_out, n_in, _ptr(x), _XTYPE[x.dtype],
+          _ptr(ids), T, k, _MODE[mode], _ptr(out), _ptr(ws))
     if own_ws:
         _chk(get_status(ws), "moe_mul_mat_id (device status)")
     return out
@@ -387,9 +388,8 @@ def ffn(Wg, Wu, Wd, n_experts, n_embd, n_ff, x, ids, shared=None, ws=None, out=N
         out_shared = torch.empty((T, n_embd), dtype=torch.float32, device=dev)
     if shared is not None:
         _need(out_shared, "out_shared", torch.float32, T * n_embd, dev)
-    _chk(_L().moe_ffn_w(w, _ptr(Wg), _ptr(Wu), _ptr(Wd), n_experts, n_embd, n_ff, _ptr(Sg), _ptr(Su), _ptr(Sd),
-                        n_ff_sh, _ptr(x), _XTYPE[x.dtype], _ptr(ids), T, k, _ptr(out), _ptr(out_shared), _ptr(ws),
-                        _stream(x.device)), "moe_ffn")
+    _call("moe_ffn", dev, _L().moe_ffn_w, w, _ptr(Wg), _ptr(Wu), _ptr(Wd), n_experts, n_embd, n_ff, _ptr(Sg), _ptr(Su),
+          _ptr(Sd), n_ff_sh, _ptr(x), _XTYPE[x.dtype], _ptr(ids), T, k, _ptr(out), _ptr(out_shared), _ptr(ws))
     if own_ws:
         _chk(get_status(ws), "moe_ffn (device status)")
     return out, out_shared
@@ -418,9 +418,9 @@ def ffn_decode_noalloc(Wg, Wu, Wd, n_experts, n_embd, n_ff, x, ids, shared=None,
         _need(out_shared, "out_shared", torch.float32, T * n_embd, dev)
     if status is not None:
         _need(status, "status", torch.int32, 1, dev)
-    _chk(_L().moe_ffn_decode_noalloc(_ptr(Wg), _ptr(Wu), _ptr(Wd), n_experts, n_embd, n_ff, _ptr(Sg), _ptr(Su),
-                                     _ptr(Sd), n_ff_sh, _ptr(x), _XTYPE[x.dtype], _ptr(ids), T, k, _ptr(out),
-                                     _ptr(out_shared), _ptr(status), _stream(x.device)), "moe_ffn_decode_noalloc")
+    _call("moe_ffn_decode_noalloc", dev, _L().moe_ffn_decode_noalloc, _ptr(Wg), _ptr(Wu), _ptr(Wd), n_experts, n_embd,
+          n_ff, _ptr(Sg), _ptr(Su), _ptr(Sd), n_ff_sh, _ptr(x), _XTYPE[x.dtype], _ptr(ids), T, k, _ptr(out),
+          _ptr(out_shared), _ptr(status))
     return out, out_shared
 
 
@@ -439,8 +439,8 @@ def route(logits, k, bias=None, normalize=True, ids=None, weights=None):
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
     _need(ids, "ids", torch.int32, T * k, dev)
     _need(weights, "weights", torch.float32, T * k, dev)
-    _chk(_L().moe_route(_ptr(logits), _ptr(bias), T, E, k, 1 if normalize else 0, _ptr(ids), _ptr(weights),
-                        _stream(logits.device)), "moe_route")
+    _call("moe_route", dev, _L().moe_route, _ptr(logits), _ptr(bias), T, E, k, 1 if normalize else 0, _ptr(ids),
+          _ptr(weights))
     return ids, weights
 
 
@@ -532,8 +532,7 @@ def combine(dst, weights, shared=None, out=None):
     if out is None:
         out = torch.empty((T, n), dtype=torch.float32, device=dev)
     _need(out, "out", torch.float32, T * n, dev)
-    _chk(_L().moe_combine(_ptr(dst), _ptr(weights), _ptr(shared), T, k, n, _ptr(out), _stream(dst.device)),
-         "moe_combine")
+    _call("moe_combine", dev, _L().moe_combine, _ptr(dst), _ptr(weights), _ptr(shared), T, k, n, _ptr(out))
     return out
 
 
